@@ -28,7 +28,9 @@ EXPORTED = ("twell_weight_norms", "twell_pack", "twell_pack_noalloc",
             "dense_ffn_ref", "sparse_ffn_bwd", "gate_preact", "twell_from_preact",
             "ell_from_preact", "sffn_probe_hbm", "sffn_probe_mfma", "sffn_probe_mfma_step",
             "sffn_probe_cached", "sffn_probe_gather", "sffn_probe_bf16_round",
-            "sffn_workspace_bytes", "sparse_ffn_bwd_workspace_bytes", "sffn_strerror")
+            "sffn_workspace_bytes", "sparse_ffn_bwd_workspace_bytes", "sffn_strerror",
+            "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes",
+            "paged_kv_append", "paged_attn_fwd", "paged_attn_workspace_bytes")
 
 
 class SffnError(RuntimeError):
@@ -40,6 +42,19 @@ class SffnError(RuntimeError):
 class Shape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("d_model", ctypes.c_int32), ("d_ff", ctypes.c_int32),
                 ("tile", ctypes.c_int32), ("cap", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "n_q_heads", "n_kv_heads", "head_dim", "rot_dim", "rot_adjacent", "max_pos",
+                 "norm")] + [("eps", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class PagedBatch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "n_seqs", "n_q_heads", "n_kv_heads", "head_dim", "page_size", "n_pages",
+                 "max_pages", "max_q", "max_kv", "causal", "window")] + \
+               [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -76,6 +91,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                "ell_from_preact", "sffn_probe_hbm", "sffn_probe_mfma", "sffn_probe_mfma_step",
                "sffn_probe_cached", "sffn_probe_gather", "sffn_probe_bf16_round"):
         getattr(lib, fn).restype = i32
+    hp, bp, i64 = ctypes.POINTER(Heads), ctypes.POINTER(PagedBatch), ctypes.c_int64
+    rows, cache = [vp, i64, i64], [vp, i64, i64, i64]
+    lib.qk_norm_rope.argtypes = [hp] + rows * 2 + [vp] * 4 + rows * 2 + [vp]
+    lib.qk_norm_rope_bwd.argtypes = [hp] + rows * 2 + [vp] * 4 + rows * 4 + [vp] * 3 + [sz, vp]
+    lib.paged_kv_append.argtypes = [hp] + rows * 3 + [vp] * 5 + rows + cache * 2 + [i32, i32, vp]
+    lib.paged_attn_fwd.argtypes = [bp] + rows + cache * 2 + [vp] * 3 + rows + [vp, vp, sz, vp]
+    for fn in ("qk_norm_rope", "qk_norm_rope_bwd", "paged_kv_append", "paged_attn_fwd"):
+        getattr(lib, fn).restype = i32
+    lib.qk_norm_rope_bwd_workspace_bytes.argtypes = [hp]
+    lib.qk_norm_rope_bwd_workspace_bytes.restype = sz
+    lib.paged_attn_workspace_bytes.argtypes = [bp]
+    lib.paged_attn_workspace_bytes.restype = sz
     lib.sffn_workspace_bytes.argtypes = [sp, i32]
     lib.sffn_workspace_bytes.restype = sz
     lib.sffn_strerror.argtypes = [i32]
@@ -329,6 +356,188 @@ def ell_from_preact(shape: Shape, width: int, z, x, wg_t, b_g, count, idx, val, 
     _check("ell_from_preact", _lib.ell_from_preact(
         ctypes.byref(shape), int(width), _ptr(z), _ptr(x), _ptr(wg_t), _ptr(b_g), _ptr(wg_norms),
         _ptr(count), _ptr(idx), _ptr(val), _ptr(workspace), ws_n, _stream(stream)))
+
+
+# ------------------------------------------------ the attention side of the block
+def _code(dtype) -> int:
+    if dtype is torch.bfloat16 or dtype == SFFN_BF16:
+        return SFFN_BF16
+    if dtype is torch.float32 or dtype == SFFN_F32:
+        return SFFN_F32
+    raise TypeError(f"unsupported dtype {dtype}: float32 or bfloat16")
+
+
+_TORCH_DTYPE = {SFFN_F32: torch.float32, SFFN_BF16: torch.bfloat16}
+
+
+def make_heads(T: int, n_q_heads: int, n_kv_heads: int, head_dim: int, dtype, rot_dim: int = 0,
+               max_pos: int = 0, norm: bool = False, eps: float = 1e-6,
+               adjacent: bool = False) -> Heads:
+    """Heads of q and k with their norm and rotation.  dtype: torch.float32 or
+    torch.bfloat16 (or the library's code); adjacent: pairs (2i, 2i+1) instead of
+    (i, i + rot_dim/2)."""
+    return Heads(int(T), int(n_q_heads), int(n_kv_heads), int(head_dim), int(rot_dim),
+                 int(bool(adjacent)), int(max_pos), int(bool(norm)), float(eps), _code(dtype))
+
+
+def make_paged_batch(T: int, n_seqs: int, n_q_heads: int, n_kv_heads: int, head_dim: int, dtype,
+                     page_size: int, n_pages: int, max_pages: int, max_q: int, max_kv: int,
+                     causal: bool = True, window: int = 0, scale: float | None = None) -> PagedBatch:
+    """A batch of sequences over a paged cache.  max_q, max_kv: upper bounds of
+    one sequence's new tokens and length; scale: default 1 / sqrt(head_dim)."""
+    return PagedBatch(int(T), int(n_seqs), int(n_q_heads), int(n_kv_heads), int(head_dim),
+                      int(page_size), int(n_pages), int(max_pages), int(max_q), int(max_kv),
+                      int(bool(causal)), int(window),
+                      float(head_dim) ** -0.5 if scale is None else float(scale), _code(dtype))
+
+
+def rotary_table(max_pos: int, rot_dim: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """cos and sin of p * theta^(-2i/rot_dim) for every position p, float32
+    [max_pos, rot_dim]: the rot_dim / 2 cosines of a position, then the sines."""
+    freq = theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / max(rot_dim, 1))
+    angle = torch.arange(max_pos, dtype=torch.float64)[:, None] * freq[None, :]
+    return torch.cat([angle.cos(), angle.sin()], 1).float().contiguous().to(device)
+
+
+def _rows(name: str, t, T: int, heads: int, dim: int, dtype):
+    """Pointer, token stride and head stride of a [T, heads, dim] view."""
+    if t is None or heads == 0:
+        return None, 0, 0
+    if t.shape != (T, heads, dim):
+        raise ValueError(f"{name} must be [{T}, {heads}, {dim}], not {list(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
+        raise ValueError(f"{name}: head_dim must be contiguous")
+    return t.data_ptr(), s0, s1
+
+
+def _cache(name: str, t, n_pages: int, page_size: int, heads: int, dim: int, dtype):
+    """Pointer and page, token and head strides of a paged cache."""
+    if t.shape != (n_pages, page_size, heads, dim):
+        raise ValueError(f"{name} must be [{n_pages}, {page_size}, {heads}, {dim}], "
+                         f"not {list(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1:
+        raise ValueError(f"{name}: head_dim must be contiguous")
+    return t.data_ptr(), s0, s1, s2
+
+
+def _array(name: str, t, n: int, dtype):
+    """Pointer of a contiguous array of at least n elements (None: absent)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.numel() < n:
+        raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _rotation(h: Heads, q_weight, k_weight, table, positions, dt):
+    if h.rot_dim and table is not None and table.dim() == 2 and table.shape[1] != h.rot_dim:
+        raise ValueError(f"the rotation table must be [max_pos, {h.rot_dim}]")
+    return (_array("q_weight", q_weight, h.head_dim, dt),
+            _array("k_weight", k_weight, h.head_dim, dt),
+            _array("the rotation table", table, h.max_pos * h.rot_dim, torch.float32),
+            _array("positions", positions, h.T, torch.int32))
+
+
+def _stream_ptr(stream) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def qk_norm_rope(heads: Heads, q, k, q_weight, k_weight, table, positions, q_out, k_out,
+                 stream=None) -> None:
+    """q_out, k_out = the heads of q and k, normalised and rotated by position."""
+    T, D, dt = heads.T, heads.head_dim, _TORCH_DTYPE[heads.dtype]
+    nq, nk = heads.n_q_heads, heads.n_kv_heads
+    _check("qk_norm_rope", _lib.qk_norm_rope(
+        heads, *_rows("q", q, T, nq, D, dt), *_rows("k", k, T, nk, D, dt),
+        *_rotation(heads, q_weight, k_weight, table, positions, dt),
+        *_rows("q_out", q_out, T, nq, D, dt), *_rows("k_out", k_out, T, nk, D, dt),
+        _stream_ptr(stream)))
+
+
+def alloc_heads_workspace(heads: Heads, device=None) -> torch.Tensor:
+    """Device workspace of qk_norm_rope_bwd."""
+    n = int(_lib.qk_norm_rope_bwd_workspace_bytes(heads))
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def qk_norm_rope_bwd(heads: Heads, q, k, q_weight, k_weight, table, positions, gq_out, gk_out, gq,
+                     gk, gq_weight, gk_weight, workspace, stream=None) -> None:
+    """gq, gk (as q, k) and the float32 weight gradients [head_dim] (each may be
+    None) from the gradients of qk_norm_rope's outputs."""
+    T, D, dt = heads.T, heads.head_dim, _TORCH_DTYPE[heads.dtype]
+    nq, nk = heads.n_q_heads, heads.n_kv_heads
+    ws, ws_n = (None, 0) if workspace is None else \
+        (_ptr(workspace), workspace.numel() * workspace.element_size())
+    _check("qk_norm_rope_bwd", _lib.qk_norm_rope_bwd(
+        heads, *_rows("q", q, T, nq, D, dt), *_rows("k", k, T, nk, D, dt),
+        *_rotation(heads, q_weight, k_weight, table, positions, dt),
+        *_rows("gq_out", gq_out, T, nq, D, dt), *_rows("gk_out", gk_out, T, nk, D, dt),
+        *_rows("gq", gq, T, nq, D, dt), *_rows("gk", gk, T, nk, D, dt),
+        _array("gq_weight", gq_weight, D, torch.float32),
+        _array("gk_weight", gk_weight, D, torch.float32), ws, ws_n, _stream_ptr(stream)))
+
+
+def paged_kv_append(heads: Heads, q, k, v, q_weight, k_weight, table, positions, slots, q_out,
+                    k_cache, v_cache, stream=None) -> None:
+    """q normalised and rotated into q_out, k into its slots of k_cache, v copied
+    into v_cache ([n_pages, page_size, n_kv_heads, head_dim], any strides).
+    slots: int32 [T], page * page_size + offset, -1: not stored.  With
+    heads.n_q_heads == 0, q and q_out may be None."""
+    T, D, dt = heads.T, heads.head_dim, _TORCH_DTYPE[heads.dtype]
+    nq, nk = heads.n_q_heads, heads.n_kv_heads
+    n_pages, page_size = k_cache.shape[0], k_cache.shape[1]
+    _check("paged_kv_append", _lib.paged_kv_append(
+        heads, *_rows("q", q, T, nq, D, dt), *_rows("k", k, T, nk, D, dt),
+        *_rows("v", v, T, nk, D, dt), *_rotation(heads, q_weight, k_weight, table, positions, dt),
+        _array("slots", slots, T, torch.int32), *_rows("q_out", q_out, T, nq, D, dt),
+        *_cache("k_cache", k_cache, n_pages, page_size, nk, D, dt),
+        *_cache("v_cache", v_cache, n_pages, page_size, nk, D, dt), n_pages, page_size,
+        _stream_ptr(stream)))
+
+
+def paged_attn_workspace_bytes(batch: PagedBatch) -> int:
+    return int(_lib.paged_attn_workspace_bytes(batch))
+
+
+def alloc_paged_workspace(batch: PagedBatch, device=None) -> torch.Tensor:
+    """Device workspace of paged_attn_fwd (no initial contents needed)."""
+    n = paged_attn_workspace_bytes(batch)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def paged_attn_fwd(batch: PagedBatch, q, k_cache, v_cache, q_start, kv_len, block_table, out,
+                   workspace, lse=None, stream=None) -> None:
+    """out [T, n_q_heads, head_dim] (and lse [T, n_q_heads] float32): attention of
+    every sequence's new tokens, rows q_start[s] .. q_start[s+1] - 1 of q, over
+    its kv_len[s] cached keys, found through block_table [n_seqs, max_pages]."""
+    T, D, dt = batch.T, batch.head_dim, _TORCH_DTYPE[batch.dtype]
+    nq, nk, ns = batch.n_q_heads, batch.n_kv_heads, batch.n_seqs
+    ws, ws_n = (None, 0) if workspace is None else \
+        (_ptr(workspace), workspace.numel() * workspace.element_size())
+    _check("paged_attn_fwd", _lib.paged_attn_fwd(
+        batch, *_rows("q", q, T, nq, D, dt),
+        *_cache("k_cache", k_cache, batch.n_pages, batch.page_size, nk, D, dt),
+        *_cache("v_cache", v_cache, batch.n_pages, batch.page_size, nk, D, dt),
+        _array("q_start", q_start, ns + 1, torch.int32), _array("kv_len", kv_len, ns, torch.int32),
+        _array("block_table", block_table, ns * batch.max_pages, torch.int32),
+        *_rows("out", out, T, nq, D, dt), _array("lse", lse, T * nq, torch.float32), ws, ws_n,
+        _stream_ptr(stream)))
 
 
 class SparseFFN:

@@ -432,6 +432,154 @@ int32_t sffn_probe_mfma_step(const void* a, const void* b, const float* c, float
  */
 int32_t sffn_probe_bf16_round(const float* in, uint16_t* out, size_t n, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The attention side of a decoder block: the heads of q and k normalised and
+ * rotated by position (training: with gradients), the keys and values of new
+ * tokens appended to a paged cache, and attention over that cache.
+ *
+ * Layouts of this part:
+ *   - q, k, v and the outputs of their shapes are [tokens, heads, head_dim]
+ *     views: a data pointer, 16-byte aligned, the element strides of a token
+ *     and of a head (multiples of 16 bytes; a stride of a dimension of size 1
+ *     is not looked at), head_dim contiguous.  So q, k and v may be slices of
+ *     one projection's output.  Outputs must not overlap themselves or inputs.
+ *   - k_cache, v_cache: [n_pages, page_size, n_kv_heads, head_dim], element
+ *     strides of a page, of a token in its page and of a head (multiples of 16
+ *     bytes; any order of these dimensions), head_dim contiguous.  Token j of a
+ *     sequence lies in page block_table[j / page_size], at j % page_size.
+ *     Offsets are 64-bit: a cache may exceed 4 GiB.
+ *   - int32 and float32 arrays: contiguous, 4-byte aligned.
+ *   - dtype applies to q, k, v, the caches, the norm weights and the outputs;
+ *     all sums, statistics and rotations are float32 and each output is rounded
+ *     once.
+ */
+
+/* Heads of q and k: their norm and rotation. */
+typedef struct {
+  int32_t T;            /* tokens; 0: nothing to do */
+  int32_t n_q_heads;    /* heads of q, may be 0 (then q, q_out, ... are NULL) */
+  int32_t n_kv_heads;   /* heads of k (and v), may be 0 except in paged_kv_append */
+  int32_t head_dim;     /* a multiple of 8, 8 .. 256 */
+  int32_t rot_dim;      /* leading elements that are rotated: a multiple of 4, 0 .. head_dim */
+  int32_t rot_adjacent; /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1) */
+  int32_t max_pos;      /* rows of rot_table */
+  int32_t norm;         /* 1: RMS norm of every head before the rotation; 0: none */
+  float eps;            /* added to the mean square, >= 0 */
+  int32_t dtype;        /* sffn_dtype */
+} sffn_heads;
+
+/*
+ * qk_norm_rope -- per-head RMS norm and position rotation of q and k in one pass:
+ *
+ *   n   = x * rsqrt(mean(x^2) + eps) * w       (norm == 1; w NULL: ones)
+ *   y_a = n_a cos - n_b sin,  y_b = n_b cos + n_a sin     for each pair (a, b)
+ *   y   = n                                    beyond rot_dim
+ *
+ * rot_table: float32 [max_pos, rot_dim]: cos of the rot_dim / 2 angles of a
+ * position, then their sin.  positions: int32 [T].  A token whose position is
+ * outside 0 .. max_pos - 1 gets NaN in its rotated elements.  Both may be NULL
+ * when rot_dim == 0.  q_weight, k_weight: [head_dim] dtype, 16-byte aligned.
+ */
+int32_t qk_norm_rope(const sffn_heads* heads, const void* q, int64_t q_token, int64_t q_head,
+                     const void* k, int64_t k_token, int64_t k_head, const void* q_weight,
+                     const void* k_weight, const float* rot_table, const int32_t* positions,
+                     void* q_out, int64_t qo_token, int64_t qo_head, void* k_out,
+                     int64_t ko_token, int64_t ko_head, void* stream);
+
+/*
+ * qk_norm_rope_bwd -- gradients of qk_norm_rope from those of its outputs.
+ *
+ *   gn = the transposed rotation of gy;  gw = sum over tokens and heads of gn * xhat
+ *   gx = r (gn w - xhat mean(gn w xhat)),  xhat = x r, r = rsqrt(mean(x^2) + eps)
+ *
+ * gq, gk: as q, k.  gq_weight, gk_weight: float32 [head_dim], each may be NULL;
+ * written (not added to), in a fixed order of summation: the same bits every
+ * time.  With norm == 0 the weight gradients are not written and x is not read
+ * (q and k may be NULL).  T == 0 writes zero weight gradients.
+ * workspace: at least qk_norm_rope_bwd_workspace_bytes(heads).
+ */
+int32_t qk_norm_rope_bwd(const sffn_heads* heads, const void* q, int64_t q_token, int64_t q_head,
+                         const void* k, int64_t k_token, int64_t k_head, const void* q_weight,
+                         const void* k_weight, const float* rot_table, const int32_t* positions,
+                         const void* gq_out, int64_t gqo_token, int64_t gqo_head,
+                         const void* gk_out, int64_t gko_token, int64_t gko_head, void* gq,
+                         int64_t gq_token, int64_t gq_head, void* gk, int64_t gk_token,
+                         int64_t gk_head, float* gq_weight, float* gk_weight, void* workspace,
+                         size_t ws_bytes, void* stream);
+size_t qk_norm_rope_bwd_workspace_bytes(const sffn_heads* heads);
+
+/*
+ * paged_kv_append -- one launch for what a serving step does before attention:
+ * q normalised and rotated into q_out, k normalised and rotated into k_cache, v
+ * copied into v_cache.  slots: int32 [T], the cache row of each token:
+ * page * page_size + offset in the page; a slot outside the cache (-1 for a
+ * padding token) is not stored.  Two tokens with one slot: which is kept is
+ * not specified.  With n_q_heads == 0 only the cache is written.
+ */
+int32_t paged_kv_append(const sffn_heads* heads, const void* q, int64_t q_token, int64_t q_head,
+                        const void* k, int64_t k_token, int64_t k_head, const void* v,
+                        int64_t v_token, int64_t v_head, const void* q_weight,
+                        const void* k_weight, const float* rot_table, const int32_t* positions,
+                        const int32_t* slots, void* q_out, int64_t qo_token, int64_t qo_head,
+                        void* k_cache, int64_t kc_page, int64_t kc_token, int64_t kc_head,
+                        void* v_cache, int64_t vc_page, int64_t vc_token, int64_t vc_head,
+                        int32_t n_pages, int32_t page_size, void* stream);
+
+/* A batch of sequences over a paged cache. */
+typedef struct {
+  int32_t T;          /* rows of q (new tokens of all sequences) */
+  int32_t n_seqs;
+  int32_t n_q_heads;  /* a multiple of n_kv_heads */
+  int32_t n_kv_heads;
+  int32_t head_dim;   /* a multiple of 8, 8 .. 256 */
+  int32_t page_size;  /* >= 1, any */
+  int32_t n_pages;    /* pages of the cache */
+  int32_t max_pages;  /* columns of block_table */
+  int32_t max_q;      /* no sequence has more new tokens */
+  int32_t max_kv;     /* no sequence is longer; at most max_pages * page_size */
+  int32_t causal;     /* 1: a token sees no later key; 0: it does */
+  int32_t window;     /* > 0: a token sees no key `window` or more before it; 0: no limit */
+  float scale;        /* of the scores, finite */
+  int32_t dtype;      /* sffn_dtype */
+} sffn_paged_batch;
+
+/*
+ * paged_attn_fwd -- attention of every sequence's new tokens over its cached keys
+ * (those of the new tokens included): chunks of prompts, drafts, single tokens,
+ * mixed in one batch.
+ *
+ *   Sequence s has the rows q_start[s] .. q_start[s + 1] - 1 of q and the keys
+ *   0 .. kv_len[s] - 1.  Its last row sits at position kv_len[s] - 1, the row
+ *   before it at the position before.  The row at position p sees key j when
+ *   (causal == 0 or j <= p) and (window == 0 or j > p - window).
+ *   out = sum_j softmax_j(scale q . k_j) v_j over the keys it sees, with query
+ *   head h on key head h / (n_q_heads / n_kv_heads);
+ *   lse = log sum_j exp(scale q . k_j).  A row that sees no key gets out = 0
+ *   and lse = -inf.
+ *
+ * q_start: int32 [n_seqs + 1], not decreasing, within 0 .. T; rows of q that
+ * belong to no sequence are not written.  kv_len: int32 [n_seqs], 0 .. max_kv.
+ * block_table: int32 [n_seqs, max_pages]; entries past a sequence's length, and
+ * pages wholly before every window, are not used; the others must lie in
+ * 0 .. n_pages - 1.  (These arrays are on the device and cannot be checked on
+ * the host: the kernels bound every value, so a wrong one gives wrong
+ * results but no access outside the buffers.)  Cache rows that a row does not
+ * see may hold anything, NaN included: they do not change its result.
+ * out: as q.  lse: float32 [T, n_q_heads] or NULL.
+ * workspace: at least paged_attn_workspace_bytes(batch); no initial contents.
+ * Weights of the bf16 softmax are rounded to bf16 before the product with v;
+ * sums and the running maximum are float32.  Results do not depend on the order
+ * in which workgroups run: the same call gives the same bits.
+ */
+int32_t paged_attn_fwd(const sffn_paged_batch* batch, const void* q, int64_t q_token,
+                       int64_t q_head, const void* k_cache, int64_t kc_page, int64_t kc_token,
+                       int64_t kc_head, const void* v_cache, int64_t vc_page, int64_t vc_token,
+                       int64_t vc_head, const int32_t* q_start, const int32_t* kv_len,
+                       const int32_t* block_table, void* out, int64_t o_token, int64_t o_head,
+                       float* lse, void* workspace, size_t ws_bytes, void* stream);
+size_t paged_attn_workspace_bytes(const sffn_paged_batch* batch);
+
 /* Workspace bytes needed by one call for this shape (0 if the shape is invalid). */
 size_t sffn_workspace_bytes(const sffn_shape* shape, int32_t which);
 
