@@ -1,0 +1,428 @@
+// Kernels of attention over a paged cache.
+//
+// The rows of a sequence under one key head are its new tokens times the query
+// heads that share the key head: row r is token r / g, head r % g, so that the
+// heads of a group share every key and value that is loaded.
+//
+//   attn_rows  many rows (chunks of prompts): four waves of 32 rows each, K and V
+//              tiles shared in LDS.
+//   attn_keys  at most 32 rows (single tokens, drafts): the waves of a workgroup
+//              hold the same rows and take the key tiles in turn, each with its
+//              own LDS and no barriers; their results are joined at the end.
+//   attn_join  joins the splits of a long key range.
+#pragma once
+
+#include "attn_tile.cuh"
+
+namespace sffn {
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // vmcnt <= N
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+
+// A sequence and the part of its rows that a workgroup takes.
+struct Work {
+  int seq, q0, nq, nkv, tile;  // tile < 0: none
+};
+
+__device__ __forceinline__ void read_sequence(const PagedAttn& p, int s, Work* w) {
+  const int a = min(max(p.q_start[s], 0), p.T), b = min(max(p.q_start[s + 1], a), p.T);
+  w->seq = s;
+  w->q0 = a;
+  w->nq = b - a;
+  w->nkv = min(max(p.kv_len[s], 0), p.max_kv);
+}
+
+// Row tile number `t` of the sequences with more than min_rows rows, in order:
+// 64 sequences a step, a prefix sum of their tiles.
+template <int TM>
+__device__ __forceinline__ Work find_tile(const AttnArgs& a, int t) {
+  const PagedAttn& p = a.p;
+  Work w;
+  w.tile = -1;
+  w.seq = w.q0 = w.nq = w.nkv = 0;
+  int base = 0;
+  for (int s0 = 0; s0 < p.n_seqs; s0 += kWave) {
+    const int s = s0 + lane_id();
+    int n = 0;
+    if (s < p.n_seqs) {
+      const int b = min(max(p.q_start[s], 0), p.T), e = min(max(p.q_start[s + 1], b), p.T);
+      const int rows = (e - b) * a.g;
+      n = rows > a.min_rows ? (rows + TM - 1) / TM : 0;
+    }
+    int up = n;  // inclusive prefix sum
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int v = __shfl_up(up, o, kWave);
+      if (lane_id() >= o) up += v;
+    }
+    const uint64_t hit = __ballot(base + up > t);
+    if (hit != 0) {
+      const int k = (int)__builtin_ctzll(hit);
+      read_sequence(p, s0 + k, &w);
+      w.tile = t - (base + __shfl(up - n, k, kWave));
+      break;
+    }
+    base += __shfl(up, kWave - 1, kWave);
+  }
+  w.seq = uniform(w.seq);
+  w.q0 = uniform(w.q0);
+  w.nq = uniform(w.nq);
+  w.nkv = uniform(w.nkv);
+  w.tile = uniform(w.tile);
+  return w;
+}
+
+// The keys [lo, hi) that token i (0 .. nq - 1) sees; lo == hi: none.
+__device__ __forceinline__ void key_range(const PagedAttn& p, const Work& w, int i, int* lo, int* hi) {
+  const int pos = w.nkv - w.nq + i;
+  *hi = p.causal ? max(pos + 1, 0) : w.nkv;
+  *lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
+  *lo = min(*lo, *hi);
+}
+
+// Keys of one split: chunk number `split` of those that the range [lo, hi) of all
+// rows touches.  Returns the number of splits of the range (at least 1).
+__device__ __forceinline__ int split_range(const AttnArgs& a, int split, int lo, int hi, int* b, int* e) {
+  if (hi <= lo) {
+    *b = *e = lo;
+    return 1;
+  }
+  const int c0 = lo / a.chunk, n = (hi - 1) / a.chunk - c0 + 1;
+  *b = max(lo, (c0 + split) * a.chunk);
+  *e = min((int64_t)hi, (int64_t)(c0 + split + 1) * a.chunk);
+  return n;
+}
+
+// Writes one row's outputs (lane: d = 8 * quad + 4 * half + 0..3 of each 32): the
+// result, or its part of a split.
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float a, float b, float c, float d) {
+  if constexpr (sizeof(T) == 2) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    u32x2 v;
+    v.x = pack_bf16(a, b);
+    v.y = pack_bf16(c, d);
+    *(u32x2*)p = v;
+  } else {
+    f32x4_t v = {a, b, c, d};
+    *(f32x4_t*)p = v;
+  }
+}
+
+__device__ __forceinline__ float finish_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
+}
+
+template <typename T, int DP, int KT, int NW, bool FAST>
+__global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void attn_rows(AttnArgs a) {
+  typedef AttnTile<T, DP, KT> Tile;
+  constexpr int TM = NW * 32;
+  extern __shared__ __align__(16) uint8_t lds[];
+  const PagedAttn& p = a.p;
+  // key heads run fastest over the workgroups, which go round the XCDs: with
+  // eight of them (or a multiple) an XCD's L2 holds the keys of one head.  The
+  // last tiles, which see most keys, start first.
+  const int hk = (int)blockIdx.x % p.hkv, t = a.n_tiles - 1 - (int)blockIdx.x / p.hkv;
+  const int split = blockIdx.y;
+  const Work w = find_tile<TM>(a, t);
+  if (w.tile < 0) return;
+  const int wave = uniform((int)threadIdx.x / kWave), lane = lane_id(), half = lane >> 5;
+  const int rows = w.nq * a.g;
+  const int r0 = w.tile * TM, r1 = min(r0 + TM, rows) - 1;  // first and last row of the tile
+  int lo, hi, b, e, x, y;
+  key_range(p, w, a.group.div(r0), &lo, &y);
+  key_range(p, w, a.group.div(r1), &x, &hi);
+  const int n_split = split_range(a, split, lo, hi, &b, &e);
+  if (split >= n_split) return;
+  // this lane's row, and the ranges of the wave's first and last row
+  const int wr0 = min(r0 + wave * 32, rows - 1), wr1 = min(wr0 + 31, r1);
+  const int r = min(r0 + wave * 32 + (lane & 31), r1);
+  const int token = a.group.div(r), head = hk * a.g + r - token * a.g;
+  int row_lo, row_hi, w_lo0, w_hi0, w_lo1, w_hi1;
+  key_range(p, w, token, &row_lo, &row_hi);
+  key_range(p, w, a.group.div(wr0), &w_lo0, &w_hi0);
+  key_range(p, w, a.group.div(wr1), &w_lo1, &w_hi1);
+  const bool wave_live = r0 + wave * 32 <= r1;
+
+  Tile tile;
+  tile.init();
+  tile.load_q((const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D, a.negate != 0);
+  if (p.D != DP || DP != Tile::kRowElems) {  // chunks that no load writes
+    for (int i = threadIdx.x; i < 4 * Tile::kTileBytes / 16; i += NW * 64)
+      ((u32x4_t*)lds)[i] = u32x4_t{0u, 0u, 0u, 0u};
+    __syncthreads();
+  }
+  constexpr int kPer = Tile::kLoads / NW;
+  static_assert(kPer >= 1, "");
+  TileLoader<T, DP, KT, FAST, kPer> loader;
+  loader.init(a, w.seq, hk, b, e, wave * kPer);
+  // keys that every row of the workgroup, of the wave sees
+  const int all_lo = x, all_hi = y;
+  int buf = 0, j0 = b & ~(KT - 1);
+  if (e > b) {
+    loader.look_up(j0);
+    loader.start(lds, lds + Tile::kTileBytes);
+    loader.look_up(j0 + KT);
+  }
+  for (; j0 < e; j0 += KT) {
+    wait_loads<0>();
+    __syncthreads();  // this tile is in LDS, and nobody reads the other one any more
+    uint8_t* k = lds + buf * 2 * Tile::kTileBytes;
+    uint8_t* v = k + Tile::kTileBytes;
+    if (j0 + KT < e) {
+      uint8_t* next = lds + (buf ^ 1) * 2 * Tile::kTileBytes;
+      loader.start(next, next + Tile::kTileBytes);
+      loader.look_up(j0 + 2 * KT);
+    }
+    if (!(j0 >= all_lo && j0 + KT <= all_hi) &&
+        __syncthreads_or(Tile::find_infinite(v, threadIdx.x, NW * 64))) {
+      tile.add_infinite(v, j0, row_lo, row_hi);
+      __syncthreads();
+      Tile::clear_infinite(v, threadIdx.x, NW * 64);
+      __syncthreads();
+    }
+    if (wave_live && j0 < w_hi1 && j0 + KT > w_lo0)
+      tile.step(k, v, j0, row_lo, row_hi, j0 >= w_lo1 && j0 + KT <= w_hi0, a.c);
+    buf ^= 1;
+  }
+  tile.l += other_half(tile.l);
+  const float m = tile.m * a.c;
+  if (r0 + wave * 32 + (lane & 31) > r1) return;
+  if (n_split == 1) {
+    const float inv = tile.l == 0.f ? 0.f : 1.f / tile.l;
+    T* out = (T*)p.out + (int64_t)(w.q0 + token) * p.o_token + head * p.o_head;
+#pragma unroll
+    for (int d = 0; d < Tile::kDt; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = d * 32 + 8 * i + 4 * half;
+        if (at < p.D)
+          store4<T>(out + at, tile.o[d][4 * i] * inv, tile.o[d][4 * i + 1] * inv,
+                    tile.o[d][4 * i + 2] * inv, tile.o[d][4 * i + 3] * inv);
+      }
+    if (p.lse != nullptr && half == 0)
+      p.lse[(int64_t)(w.q0 + token) * p.hq + head] = finish_lse(m, tile.l);
+  } else {
+    const size_t slot = split * a.part_rows + ((size_t)t * p.hkv + hk) * TM + (r - r0);
+    float* out = a.part_o + slot * p.D;
+#pragma unroll
+    for (int d = 0; d < Tile::kDt; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = d * 32 + 8 * i + 4 * half;
+        if (at < p.D)
+          store4<float>(out + at, tile.o[d][4 * i], tile.o[d][4 * i + 1], tile.o[d][4 * i + 2],
+                        tile.o[d][4 * i + 3]);
+      }
+    if (half == 0) {
+      a.part_ml[2 * slot] = m;
+      a.part_ml[2 * slot + 1] = tile.l;
+    }
+  }
+}
+
+template <typename T, int DP, int NW, bool FAST>
+__global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
+  constexpr int KT = 32;
+  typedef AttnTile<T, DP, KT> Tile;
+  extern __shared__ __align__(16) uint8_t lds[];
+  const PagedAttn& p = a.p;
+  const int hk = (int)blockIdx.x % p.hkv, split = blockIdx.y;
+  Work w;
+  read_sequence(p, (int)blockIdx.x / p.hkv, &w);
+  const int rows = w.nq * a.g;
+  if (rows == 0 || rows > 32) return;
+  const int wave = uniform((int)threadIdx.x / kWave), lane = lane_id(), half = lane >> 5;
+  int lo, hi, b, e, x, y;
+  key_range(p, w, 0, &lo, &y);
+  key_range(p, w, w.nq - 1, &x, &hi);
+  const int n_split = split_range(a, split, lo, hi, &b, &e);
+  if (split >= n_split) return;
+  const int r = min(lane & 31, rows - 1);
+  const int token = a.group.div(r), head = hk * a.g + r - token * a.g;
+  int row_lo, row_hi;
+  key_range(p, w, token, &row_lo, &row_hi);
+  Tile tile;
+  tile.init();
+  tile.load_q((const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D, a.negate != 0);
+  uint8_t* mine = lds + wave * 4 * Tile::kTileBytes;
+  if (p.D != DP || DP != Tile::kRowElems)
+    for (int i = lane; i < 4 * Tile::kTileBytes / 16; i += kWave)
+      ((u32x4_t*)mine)[i] = u32x4_t{0u, 0u, 0u, 0u};
+  TileLoader<T, DP, KT, FAST, Tile::kLoads> loader;
+  loader.init(a, w.seq, hk, b, e, 0);
+  int buf = 0, j0 = (b & ~(KT - 1)) + wave * KT;
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // the zeros are written (lgkmcnt)
+  if (j0 < e) {
+    loader.look_up(j0);
+    loader.start(mine, mine + Tile::kTileBytes);
+    loader.look_up(j0 + NW * KT);
+  }
+  for (; j0 < e; j0 += NW * KT) {
+    wait_loads<0>();
+    uint8_t* k = mine + buf * 2 * Tile::kTileBytes;
+    uint8_t* v = k + Tile::kTileBytes;
+    if (j0 + NW * KT < e) {
+      uint8_t* next = mine + (buf ^ 1) * 2 * Tile::kTileBytes;
+      loader.start(next, next + Tile::kTileBytes);
+      loader.look_up(j0 + 2 * NW * KT);
+    }
+    const bool whole = j0 >= x && j0 + KT <= y;
+    if (!whole && __any(Tile::find_infinite(v, lane, kWave))) {
+      tile.add_infinite(v, j0, row_lo, row_hi);
+      Tile::clear_infinite(v, lane, kWave);
+    }
+    tile.step(k, v, j0, row_lo, row_hi, whole, a.c);
+    buf ^= 1;
+  }
+  tile.l += other_half(tile.l);
+  // join the waves: each leaves its rows in LDS, [row][d] with a pitch that keeps
+  // 16-byte writes of neighbouring rows apart
+  constexpr int kPitchO = DP + 4;
+  __syncthreads();
+  float* po = (float*)lds;  // [NW][32][kPitchO], then [NW][32][2]
+  float* pm = po + NW * 32 * kPitchO;
+  {
+    float* row = po + (wave * 32 + (lane & 31)) * kPitchO;
+#pragma unroll
+    for (int d = 0; d < Tile::kDt; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        store4<float>(row + d * 32 + 8 * i + 4 * half, tile.o[d][4 * i], tile.o[d][4 * i + 1],
+                      tile.o[d][4 * i + 2], tile.o[d][4 * i + 3]);
+    if (half == 0) {
+      pm[(wave * 32 + (lane & 31)) * 2] = tile.m * a.c;
+      pm[(wave * 32 + (lane & 31)) * 2 + 1] = tile.l;
+    }
+  }
+  __syncthreads();
+  const int quads = p.D / 4;
+  for (int i = threadIdx.x; i < rows * quads; i += NW * 64) {
+    const int rr = i / quads, d = (i - rr * quads) * 4;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) m = fmaxf(m, pm[(k * 32 + rr) * 2]);
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const float mk = pm[(k * 32 + rr) * 2];
+      const float f = mk == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mk - m);
+      l += f * pm[(k * 32 + rr) * 2 + 1];
+      if (mk != -INFINITY) v += f * *(const f32x4_t*)(po + (k * 32 + rr) * kPitchO + d);
+    }
+    const int tk = a.group.div(rr), hd = hk * a.g + rr - tk * a.g;
+    if (n_split == 1) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      store4<T>((T*)p.out + (int64_t)(w.q0 + tk) * p.o_token + hd * p.o_head + d, v[0] * inv,
+                v[1] * inv, v[2] * inv, v[3] * inv);
+      if (d == 0 && p.lse != nullptr) p.lse[(int64_t)(w.q0 + tk) * p.hq + hd] = finish_lse(m, l);
+    } else {
+      const size_t slot = split * a.part_rows + (size_t)blockIdx.x * 32 + rr;
+      *(f32x4_t*)(a.part_o + slot * p.D + d) = v;
+      if (d == 0) {
+        a.part_ml[2 * slot] = m;
+        a.part_ml[2 * slot + 1] = l;
+      }
+    }
+  }
+}
+
+// Joins the splits of the rows of one tile (TM rows; 32: attn_keys' sequences):
+// a thread holds four elements of a row.
+template <typename T, int TM>
+__global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
+  const PagedAttn& p = a.p;
+  const int hk = (int)blockIdx.x % p.hkv, t = (int)blockIdx.x / p.hkv;
+  Work w;
+  if constexpr (TM == 32) {
+    read_sequence(p, t, &w);
+    w.tile = 0;
+    if (w.nq == 0 || w.nq * a.g > 32) return;
+  } else {
+    w = find_tile<TM>(a, t);
+    if (w.tile < 0) return;
+  }
+  const int rows = w.nq * a.g, r0 = w.tile * TM, r1 = min(r0 + TM, rows) - 1;
+  int lo, hi, b, e, x, y;
+  key_range(p, w, a.group.div(r0), &lo, &y);
+  key_range(p, w, a.group.div(r1), &x, &hi);
+  const int n = split_range(a, 0, lo, hi, &b, &e);
+  if (n == 1) return;  // written by the kernel before
+  const int quads = p.D / 4;
+  const int part = (int)blockIdx.y * 256 + threadIdx.x;
+  for (int i = part; i < (r1 - r0 + 1) * quads; i += (int)gridDim.y * 256) {
+    const int rr = i / quads, d = (i - rr * quads) * 4;
+    const size_t slot = ((size_t)t * p.hkv + hk) * TM + rr;
+    float m = -INFINITY, l = 0.f;
+    for (int s = 0; s < n; ++s) m = fmaxf(m, a.part_ml[2 * (s * a.part_rows + slot)]);
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < n; ++s) {
+      const size_t at = s * a.part_rows + slot;
+      const float ms = a.part_ml[2 * at];
+      if (ms == -INFINITY) continue;
+      const float f = __builtin_amdgcn_exp2f(ms - m);
+      l += f * a.part_ml[2 * at + 1];
+      v += f * *(const f32x4_t*)(a.part_o + at * p.D + d);
+    }
+    const int token = a.group.div(r0 + rr), head = hk * a.g + r0 + rr - token * a.g;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    store4<T>((T*)p.out + (int64_t)(w.q0 + token) * p.o_token + head * p.o_head + d, v[0] * inv,
+              v[1] * inv, v[2] * inv, v[3] * inv);
+    if (d == 0 && p.lse != nullptr) p.lse[(int64_t)(w.q0 + token) * p.hq + head] = finish_lse(m, l);
+  }
+}
+
+// Launches of one element type, in files of their own.
+template <typename T> hipError_t launch_attn_rows(const AttnArgs& a, int splits, bool fast, hipStream_t s);
+template <typename T> hipError_t launch_attn_keys(const AttnArgs& a, int splits, bool fast, hipStream_t s);
+
+// Key tile and waves of attn_rows, waves of attn_keys, and the bytes of LDS.
+template <typename T, int DP> struct RowsShape {
+  static constexpr int kWaves = 4;
+  static constexpr int kKeys = sizeof(T) == 2 && DP <= 128 ? 64 : 32;
+  static constexpr size_t kLds = 4 * (size_t)AttnTile<T, DP, kKeys>::kTileBytes;
+};
+template <typename T, int DP> struct KeysShape {
+  static constexpr int kWaves = sizeof(T) == 4 && DP > 128 ? 1 : 2;
+  static constexpr size_t kTiles = kWaves * 4 * (size_t)AttnTile<T, DP, 32>::kTileBytes;
+  static constexpr size_t kJoin = (size_t)kWaves * 32 * (DP + 4 + 2) * 4;
+  static constexpr size_t kLds = kTiles > kJoin ? kTiles : kJoin;
+};
+
+#define SFFN_ATTN_BY_WIDTH(F, T, ...)                  \
+  do {                                                 \
+    const int d_ = a.p.D;                              \
+    if (d_ <= 64) return F<T, 64>(__VA_ARGS__);        \
+    if (d_ <= 96) return F<T, 96>(__VA_ARGS__);        \
+    if (d_ <= 128) return F<T, 128>(__VA_ARGS__);      \
+    if (d_ <= 192) return F<T, 192>(__VA_ARGS__);      \
+    return F<T, 256>(__VA_ARGS__);                     \
+  } while (0)
+
+template <typename T, int DP>
+hipError_t attn_rows_width(const AttnArgs& a, int splits, bool fast, hipStream_t s) {
+  typedef RowsShape<T, DP> S;
+  const dim3 grid((unsigned)(a.n_tiles * a.p.hkv), (unsigned)splits);
+  if (fast)
+    hipLaunchKernelGGL((attn_rows<T, DP, S::kKeys, S::kWaves, true>), grid, dim3(S::kWaves * 64),
+                       S::kLds, s, a);
+  else
+    hipLaunchKernelGGL((attn_rows<T, DP, S::kKeys, S::kWaves, false>), grid, dim3(S::kWaves * 64),
+                       S::kLds, s, a);
+  return hipGetLastError();
+}
+
+template <typename T, int DP>
+hipError_t attn_keys_width(const AttnArgs& a, int splits, bool fast, hipStream_t s) {
+  typedef KeysShape<T, DP> S;
+  const dim3 grid((unsigned)(a.p.n_seqs * a.p.hkv), (unsigned)splits);
+  if (fast)
+    hipLaunchKernelGGL((attn_keys<T, DP, S::kWaves, true>), grid, dim3(S::kWaves * 64), S::kLds, s, a);
+  else
+    hipLaunchKernelGGL((attn_keys<T, DP, S::kWaves, false>), grid, dim3(S::kWaves * 64), S::kLds, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace sffn

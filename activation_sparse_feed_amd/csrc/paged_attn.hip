@@ -1,95 +1,147 @@
-// Attention of new tokens over a paged cache.
+// Attention of new tokens over a paged cache: which kernels a batch takes, how
+// far its key ranges are split, the workspace of the splits.
 #include <hip/hip_runtime.h>
 
-#include "attn.h"
-#include "common.cuh"
+#include "attn_kernels.cuh"
 
 namespace sffn {
 
+template <> hipError_t launch_attn_rows<uint16_t>(const AttnArgs&, int, bool, hipStream_t);
+template <> hipError_t launch_attn_rows<float>(const AttnArgs&, int, bool, hipStream_t);
+template <> hipError_t launch_attn_keys<uint16_t>(const AttnArgs&, int, bool, hipStream_t);
+template <> hipError_t launch_attn_keys<float>(const AttnArgs&, int, bool, hipStream_t);
+
 namespace {
 
-// One wave per (token, query head), 64 keys at a time: each lane the score of
-// one key, then each lane up to four output elements over the 64 keys.
+constexpr int kRowsTile = 128;  // rows of an attn_rows workgroup
+constexpr int kKeysRows = 32;   // rows of an attn_keys workgroup
+constexpr int kCus = 256;
+
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// What one launch takes: workgroups without splits, splits, workspace.
+struct Plan {
+  bool used;
+  int tiles, min_rows, chunk, splits;
+  size_t part_rows, bytes;
+};
+
+// Keys that the rows of one tile of `tokens` tokens can see.
+int64_t key_span(const PagedAttn& p, int64_t tokens) {
+  if (p.window == 0) return p.max_kv;
+  const int64_t w = (int64_t)p.window + (p.causal ? tokens - 1 : p.max_q - 1);
+  return w < p.max_kv ? w : p.max_kv;
+}
+
+// Splits of a key range of at most `span` keys for `groups` workgroups: enough to
+// put `want` workgroups on the GPU, but at least `least` keys each.
+void split(Plan* pl, const PagedAttn& p, int64_t span, int64_t groups, int64_t want, int least, int most) {
+  int64_t n = groups > 0 ? (want + groups - 1) / groups : 1;
+  int64_t chunk = (span + n - 1) / n;
+  if (chunk < least) chunk = least;
+  if (chunk > most) chunk = most;
+  chunk = (chunk + 63) / 64 * 64;
+  pl->chunk = (int)chunk;
+  // a range that does not start at a multiple of the chunk touches one more
+  pl->splits = (int)((span + chunk - 1) / chunk) + (p.window > 0 ? 1 : 0);
+  if (pl->splits < 1) pl->splits = 1;
+  pl->bytes = pl->splits > 1 ? align256((size_t)pl->splits * pl->part_rows * p.D * 4) +
+                                   align256((size_t)pl->splits * pl->part_rows * 8)
+                             : 0;
+}
+
+Plan plan_keys(const PagedAttn& p) {
+  Plan pl = {};
+  const int g = p.hq / p.hkv;
+  // one sequence with more rows than fit goes to attn_rows alone
+  pl.used = g <= kKeysRows && (p.n_seqs > 1 || (int64_t)p.max_q * g <= kKeysRows);
+  if (!pl.used) return pl;
+  pl.tiles = p.n_seqs;
+  pl.part_rows = (size_t)p.n_seqs * p.hkv * kKeysRows;
+  split(&pl, p, key_span(p, kKeysRows / g), (int64_t)p.n_seqs * p.hkv, 4 * kCus, 256, 2048);
+  return pl;
+}
+
+Plan plan_rows(const PagedAttn& p, bool with_keys) {
+  Plan pl = {};
+  const int g = p.hq / p.hkv;
+  pl.min_rows = with_keys ? kKeysRows : 0;
+  pl.used = (int64_t)p.max_q * g > pl.min_rows;
+  if (!pl.used) return pl;
+  const int64_t rows = (int64_t)p.T * g;
+  // every taken sequence has at most one tile that is not full
+  int64_t part = rows / (pl.min_rows + 1);
+  if (part > p.n_seqs) part = p.n_seqs;
+  pl.tiles = (int)(rows / kRowsTile + part);
+  pl.part_rows = (size_t)pl.tiles * p.hkv * kRowsTile;
+  split(&pl, p, key_span(p, kRowsTile / g + 2), (int64_t)pl.tiles * p.hkv, 2 * kCus, 512, 1 << 30);
+  return pl;
+}
+
+void place(AttnArgs* a, const Plan& pl, void* ws) {
+  a->chunk = pl.chunk;
+  a->min_rows = pl.min_rows;
+  a->n_tiles = pl.tiles;
+  a->part_rows = pl.part_rows;
+  a->part_o = (float*)ws;
+  a->part_ml = (float*)((char*)ws + align256((size_t)pl.splits * pl.part_rows * a->p.D * 4));
+}
+
 template <typename T>
-__global__ __launch_bounds__(64) void attn_simple(PagedAttn p) {
-  const int lane = lane_id();
-  const int t = blockIdx.x, h = blockIdx.y;
-  // the sequence that owns row t
-  int s = -1, q0 = 0, q1 = 0;
-  for (int i = 0; i < p.n_seqs; ++i) {
-    const int a = max(0, p.q_start[i]), b = min(p.T, p.q_start[i + 1]);
-    if (t >= a && t < b) {
-      s = i, q0 = a, q1 = b;
-      break;
+hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipStream_t s) {
+  const PagedAttn& p = a.p;
+  // see TileLoader: granules of 16 rows in one page, full LDS rows, and lane
+  // offsets of less than 32 rows in 32 bits
+  const bool fast = (p.D == 64 || p.D == 128 || p.D == 256) && p.page_size % 16 == 0 &&
+                    p.kc_token < (1 << 24) && p.vc_token < (1 << 24);
+  hipError_t e = hipSuccess;
+  const unsigned join_y = (unsigned)((p.D + 31) / 32);
+  if (rows.used) {
+    place(&a, rows, (char*)ws + keys.bytes);
+    e = launch_attn_rows<T>(a, rows.splits, fast, s);
+    if (e != hipSuccess) return e;
+    if (rows.splits > 1) {
+      hipLaunchKernelGGL((attn_join<T, kRowsTile>), dim3((unsigned)(rows.tiles * p.hkv), join_y),
+                         dim3(256), 0, s, a);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
     }
   }
-  if (s < 0) return;
-  const int nkv = max(0, min(min(p.kv_len[s], p.max_kv), p.max_pages * p.page_size));
-  const int pos = nkv - (q1 - q0) + (t - q0);
-  const int hi = p.causal ? min(nkv, pos + 1) : nkv;
-  const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-  const int hk = h / (p.hq / p.hkv);
-  const int32_t* bt = p.block_table + (size_t)s * p.max_pages;
-  __shared__ float qs[256];
-  for (int d = lane; d < p.D; d += kWave)
-    qs[d] = Elt<T>::load1(p.q, (size_t)(t * p.q_token + h * p.q_head + d)) * p.scale;
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int j0 = lo; j0 < hi; j0 += kWave) {
-    const int j = j0 + lane;
-    float sc = -INFINITY;
-    if (j < hi) {
-      const int page = min(max(bt[j / p.page_size], 0), p.n_pages - 1);
-      const size_t at = (size_t)(page * p.kc_page + (j % p.page_size) * p.kc_token + hk * p.kc_head);
-      sc = 0.f;
-      for (int d = 0; d < p.D; d += Elt<T>::kPerChunk) {
-        float k[Elt<T>::kPerChunk];
-        Elt<T>::unpack(ldg16((const T*)p.k_cache + at + d), k);
-#pragma unroll
-        for (int i = 0; i < Elt<T>::kPerChunk; ++i) sc += k[i] * qs[d + i];
-      }
-    }
-    float mx = sc;
-#pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor(mx, x, kWave));
-    const float mn = fmaxf(m, mx);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float f = __expf(m - base), w = __expf(sc - base);
-    l = l * f + wave_sum(w);
-    m = mn;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] *= f;
-    const int n = min(kWave, hi - j0);
-    for (int k = 0; k < n; ++k) {
-      const int jj = j0 + k;
-      const float wk = __shfl(w, k, kWave);
-      const int page = min(max(bt[jj / p.page_size], 0), p.n_pages - 1);
-      const size_t at = (size_t)(page * p.vc_page + (jj % p.page_size) * p.vc_token + hk * p.vc_head);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = lane + i * kWave;
-        if (d < p.D) o[i] += wk * Elt<T>::load1(p.v_cache, at + d);
-      }
+  if (keys.used) {
+    place(&a, keys, ws);
+    e = launch_attn_keys<T>(a, keys.splits, fast, s);
+    if (e != hipSuccess) return e;
+    if (keys.splits > 1) {
+      hipLaunchKernelGGL((attn_join<T, kKeysRows>), dim3((unsigned)(p.n_seqs * p.hkv), 1), dim3(256),
+                         0, s, a);
+      e = hipGetLastError();
     }
   }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int d = lane + i * kWave;
-    if (d < p.D) Elt<T>::store1(p.out, (size_t)(t * p.o_token + h * p.o_head + d), o[i] * inv);
-  }
-  if (p.lse != nullptr && lane == 0) p.lse[(size_t)t * p.hq + h] = l == 0.f ? -INFINITY : m + __logf(l);
+  return e;
 }
 
 }  // namespace
 
-size_t paged_attn_workspace(int dtype, const PagedAttn& p) { return 0; }
+size_t paged_attn_workspace(int dtype, const PagedAttn& p) {
+  if (p.T == 0 || p.n_seqs == 0 || p.max_q == 0) return 0;
+  const Plan keys = plan_keys(p);
+  return keys.bytes + plan_rows(p, keys.used).bytes;
+}
 
 hipError_t launch_paged_attn(int dtype, const PagedAttn& p, void* ws, hipStream_t stream) {
-  const dim3 grid((unsigned)p.T, (unsigned)p.hq);
-  if (dtype == 1) hipLaunchKernelGGL(attn_simple<uint16_t>, grid, dim3(64), 0, stream, p);
-  else hipLaunchKernelGGL(attn_simple<float>, grid, dim3(64), 0, stream, p);
-  return hipGetLastError();
+  const Plan keys = plan_keys(p), rows = plan_rows(p, keys.used);
+  AttnArgs a = {};
+  a.p = p;
+  a.g = p.hq / p.hkv;
+  a.page = FastDiv::make(p.page_size);
+  a.group = FastDiv::make(a.g);
+  // scores are scaled in the exponent; a scale of 0 becomes one that leaves every
+  // weight 1 but keeps hidden keys at -inf
+  const float c = (p.scale < 0.f ? -p.scale : p.scale) * 1.44269504088896340736f;
+  a.c = c > 0x1p-90f ? c : 0x1p-90f;
+  a.negate = p.scale < 0.f;
+  return dtype == 1 ? launch<uint16_t>(a, keys, rows, ws, stream)
+                    : launch<float>(a, keys, rows, ws, stream);
 }
 
 }  // namespace sffn
