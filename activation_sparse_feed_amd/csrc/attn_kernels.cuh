@@ -6,9 +6,9 @@
 //
 //   attn_rows  many rows (chunks of prompts): four waves of 32 rows each, K and V
 //              tiles shared in LDS.
-//   attn_keys  at most 32 rows (single tokens, drafts): the waves of a workgroup
-//              hold the same rows and take the key tiles in turn, each with its
-//              own LDS and no barriers; their results are joined at the end.
+//   attn_keys  few rows (single tokens, drafts): the waves of a workgroup hold the
+//              same 32 rows and take the key tiles in turn, each with its own
+//              LDS and no barriers; their results are joined at the end.
 //   attn_join  joins the splits of a long key range.
 #pragma once
 
@@ -71,6 +71,18 @@ __device__ __forceinline__ Work find_tile(const AttnArgs& a, int t) {
   w.nq = uniform(w.nq);
   w.nkv = uniform(w.nkv);
   w.tile = uniform(w.tile);
+  return w;
+}
+
+// attn_keys' tile number t: every sequence has tiles_per_seq of them, taken where
+// it has so many rows, and at most max_rows.
+__device__ __forceinline__ Work sequence_tile(const AttnArgs& a, int t) {
+  Work w;
+  const int s = t / a.tiles_per_seq;
+  read_sequence(a.p, s, &w);
+  const int rows = w.nq * a.g;
+  w.tile = t - s * a.tiles_per_seq;
+  if (w.tile * 32 >= rows || rows > a.max_rows) w.tile = -1;
   return w;
 }
 
@@ -229,18 +241,17 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
   typedef AttnTile<T, DP, KT> Tile;
   extern __shared__ __align__(16) uint8_t lds[];
   const PagedAttn& p = a.p;
-  const int hk = (int)blockIdx.x % p.hkv, split = blockIdx.y;
-  Work w;
-  read_sequence(p, (int)blockIdx.x / p.hkv, &w);
-  const int rows = w.nq * a.g;
-  if (rows == 0 || rows > 32) return;
+  const int hk = (int)blockIdx.x % p.hkv, split = blockIdx.y, t = (int)blockIdx.x / p.hkv;
+  const Work w = sequence_tile(a, t);
+  if (w.tile < 0) return;
+  const int r0 = w.tile * 32, rows = min(32, w.nq * a.g - r0);
   const int wave = uniform((int)threadIdx.x / kWave), lane = lane_id(), half = lane >> 5;
   int lo, hi, b, e, x, y;
-  key_range(p, w, 0, &lo, &y);
-  key_range(p, w, w.nq - 1, &x, &hi);
+  key_range(p, w, a.group.div(r0), &lo, &y);
+  key_range(p, w, a.group.div(r0 + rows - 1), &x, &hi);
   const int n_split = split_range(a, split, lo, hi, &b, &e);
   if (split >= n_split) return;
-  const int r = min(lane & 31, rows - 1);
+  const int r = r0 + min(lane & 31, rows - 1);
   const int token = a.group.div(r), head = hk * a.g + r - token * a.g;
   int row_lo, row_hi;
   key_range(p, w, token, &row_lo, &row_hi);
@@ -312,7 +323,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
       l += f * pm[(k * 32 + rr) * 2 + 1];
       if (mk != -INFINITY) v += f * *(const f32x4_t*)(po + (k * 32 + rr) * kPitchO + d);
     }
-    const int tk = a.group.div(rr), hd = hk * a.g + rr - tk * a.g;
+    const int tk = a.group.div(r0 + rr), hd = hk * a.g + r0 + rr - tk * a.g;
     if (n_split == 1) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
       store4<T>((T*)p.out + (int64_t)(w.q0 + tk) * p.o_token + hd * p.o_head + d, v[0] * inv,
@@ -329,48 +340,55 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
   }
 }
 
-// Joins the splits of the rows of one tile (TM rows; 32: attn_keys' sequences):
-// a thread holds four elements of a row.
+// Joins the splits of the rows of one tile (TM rows; 32: of attn_keys), a wave for
+// each row: its lanes hold the maxima and sums of up to 64 splits, then D / 4 lanes
+// a split's outputs, several splits side by side.
 template <typename T, int TM>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   const PagedAttn& p = a.p;
   const int hk = (int)blockIdx.x % p.hkv, t = (int)blockIdx.x / p.hkv;
-  Work w;
-  if constexpr (TM == 32) {
-    read_sequence(p, t, &w);
-    w.tile = 0;
-    if (w.nq == 0 || w.nq * a.g > 32) return;
-  } else {
-    w = find_tile<TM>(a, t);
-    if (w.tile < 0) return;
-  }
+  const Work w = TM == 32 ? sequence_tile(a, t) : find_tile<TM>(a, t);
+  if (w.tile < 0) return;
   const int rows = w.nq * a.g, r0 = w.tile * TM, r1 = min(r0 + TM, rows) - 1;
   int lo, hi, b, e, x, y;
   key_range(p, w, a.group.div(r0), &lo, &y);
   key_range(p, w, a.group.div(r1), &x, &hi);
   const int n = split_range(a, 0, lo, hi, &b, &e);
   if (n == 1) return;  // written by the kernel before
-  const int quads = p.D / 4;
-  const int part = (int)blockIdx.y * 256 + threadIdx.x;
-  for (int i = part; i < (r1 - r0 + 1) * quads; i += (int)gridDim.y * 256) {
-    const int rr = i / quads, d = (i - rr * quads) * 4;
-    const size_t slot = ((size_t)t * p.hkv + hk) * TM + rr;
-    float m = -INFINITY, l = 0.f;
-    for (int s = 0; s < n; ++s) m = fmaxf(m, a.part_ml[2 * (s * a.part_rows + slot)]);
-    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < n; ++s) {
-      const size_t at = s * a.part_rows + slot;
-      const float ms = a.part_ml[2 * at];
-      if (ms == -INFINITY) continue;
-      const float f = __builtin_amdgcn_exp2f(ms - m);
-      l += f * a.part_ml[2 * at + 1];
-      v += f * *(const f32x4_t*)(a.part_o + at * p.D + d);
+  const int lane = lane_id();
+  int width = 1;  // lanes of one split's outputs
+  while (width * 4 < p.D) width *= 2;
+  const int side = kWave / width, sub = lane / width, d = (lane & (width - 1)) * 4;
+  for (int r = r0 + (int)blockIdx.y * 4 + (int)threadIdx.x / kWave; r <= r1; r += (int)gridDim.y * 4) {
+    const size_t slot = ((size_t)t * p.hkv + hk) * TM + (r - r0);
+    float ms = -INFINITY, ls = 0.f;
+    if (lane < n) {
+      const size_t at = lane * a.part_rows + slot;
+      ms = a.part_ml[2 * at];
+      ls = a.part_ml[2 * at + 1];
     }
-    const int token = a.group.div(r0 + rr), head = hk * a.g + r0 + rr - token * a.g;
+    float m = ms;
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
+    const float f = ms == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms - m);
+    const float l = wave_sum(f * ls);
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    const float* o = a.part_o + slot * p.D + d;
+#pragma unroll 4
+    for (int s = sub; s - sub < n; s += side) {
+      const float fs = __shfl(f, s & (kWave - 1), kWave);
+      if (s < n && fs != 0.f && d < p.D) v += fs * *(const f32x4_t*)(o + (size_t)s * a.part_rows * p.D);
+    }
+    for (int k = width; k < kWave; k <<= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], k, kWave);
+    const int token = a.group.div(r), head = hk * a.g + r - token * a.g;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    store4<T>((T*)p.out + (int64_t)(w.q0 + token) * p.o_token + head * p.o_head + d, v[0] * inv,
-              v[1] * inv, v[2] * inv, v[3] * inv);
-    if (d == 0 && p.lse != nullptr) p.lse[(int64_t)(w.q0 + token) * p.hq + head] = finish_lse(m, l);
+    if (sub == 0 && d < p.D)
+      store4<T>((T*)p.out + (int64_t)(w.q0 + token) * p.o_token + head * p.o_head + d, v[0] * inv,
+                v[1] * inv, v[2] * inv, v[3] * inv);
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[(int64_t)(w.q0 + token) * p.hq + head] = finish_lse(m, l);
   }
 }
 
@@ -417,7 +435,7 @@ hipError_t attn_rows_width(const AttnArgs& a, int splits, bool fast, hipStream_t
 template <typename T, int DP>
 hipError_t attn_keys_width(const AttnArgs& a, int splits, bool fast, hipStream_t s) {
   typedef KeysShape<T, DP> S;
-  const dim3 grid((unsigned)(a.p.n_seqs * a.p.hkv), (unsigned)splits);
+  const dim3 grid((unsigned)(a.n_tiles * a.p.hkv), (unsigned)splits);
   if (fast)
     hipLaunchKernelGGL((attn_keys<T, DP, S::kWaves, true>), grid, dim3(S::kWaves * 64), S::kLds, s, a);
   else

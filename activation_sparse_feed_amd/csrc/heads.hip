@@ -336,21 +336,21 @@ __global__ __launch_bounds__(kHeadsBlock) void heads_bwd(HeadsBwd p) {
   }
 }
 
-// Column sums of the partials, n rows of 2 D: 16 columns per workgroup, 16
-// threads a column, in a fixed order.
+// Column sums of the partials, n rows of 2 D: 8 columns per workgroup, 32 threads
+// a column, in a fixed order.
 __global__ __launch_bounds__(256) void heads_gw_reduce(const float* __restrict__ part, int n, int D,
                                                        float* gq_weight, float* gk_weight) {
-  __shared__ float red[16][17];
-  const int col = (int)blockIdx.x * 16 + (threadIdx.x & 15), row = threadIdx.x >> 4;
+  __shared__ float red[32][9];
+  const int c = threadIdx.x & 7, row = threadIdx.x >> 3, col = (int)blockIdx.x * 8 + c;  // 2 D % 8 == 0
   float v = 0.f;
-  if (col < 2 * D)
-    for (int i = row; i < n; i += 16) v += part[(size_t)i * 2 * D + col];
-  red[row][threadIdx.x & 15] = v;
+#pragma unroll 8
+  for (int i = row; i < n; i += 32) v += part[(size_t)i * 2 * D + col];
+  red[row][c] = v;
   __syncthreads();
-  if (row == 0 && col < 2 * D) {
+  if (row == 0) {
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t += red[i][threadIdx.x & 15];
+    for (int i = 0; i < 32; ++i) t += red[i][c];
     float* out = col < D ? gq_weight : gk_weight;
     if (out != nullptr) out[col % D] = t;
   }
@@ -436,7 +436,7 @@ hipError_t launch_heads_bwd(int dtype, HeadsBwd p, bool weights, float* gq_weigh
     if (e != hipSuccess) return e;
   }
   if (!weights) return hipSuccess;
-  hipLaunchKernelGGL(heads_gw_reduce, dim3((unsigned)((2 * p.D + 15) / 16)), dim3(256), 0, stream,
+  hipLaunchKernelGGL(heads_gw_reduce, dim3((unsigned)(2 * p.D / 8)), dim3(256), 0, stream,
                      p.partial, n, p.D, gq_weight, gk_weight);
   return hipGetLastError();
 }

@@ -14,19 +14,21 @@ template <> hipError_t launch_attn_keys<float>(const AttnArgs&, int, bool, hipSt
 namespace {
 
 constexpr int kRowsTile = 128;  // rows of an attn_rows workgroup
-constexpr int kKeysRows = 32;   // rows of an attn_keys workgroup
+constexpr int kKeysTile = 32;   // rows of an attn_keys workgroup
+constexpr int kKeysMax = 64;    // rows of a sequence that attn_keys takes
 constexpr int kCus = 256;
+constexpr int kMaxSplits = 64;  // lanes of the join
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// What one launch takes: workgroups without splits, splits, workspace.
+// What one launch takes: row tiles, splits, workspace.
 struct Plan {
   bool used;
-  int tiles, min_rows, chunk, splits;
+  int tiles, tiles_per_seq, min_rows, max_rows, chunk, splits;
   size_t part_rows, bytes;
 };
 
-// Keys that the rows of one tile of `tokens` tokens can see.
+// Keys that the rows of one tile of at most `tokens` tokens can see.
 int64_t key_span(const PagedAttn& p, int64_t tokens) {
   if (p.window == 0) return p.max_kv;
   const int64_t w = (int64_t)p.window + (p.causal ? tokens - 1 : p.max_q - 1);
@@ -37,50 +39,60 @@ int64_t key_span(const PagedAttn& p, int64_t tokens) {
 // put `want` workgroups on the GPU, but at least `least` keys each.
 void split(Plan* pl, const PagedAttn& p, int64_t span, int64_t groups, int64_t want, int least, int most) {
   int64_t n = groups > 0 ? (want + groups - 1) / groups : 1;
+  // a range that does not start at a multiple of the chunk touches one more
+  const int64_t most_splits = p.window > 0 ? kMaxSplits - 1 : kMaxSplits;
   int64_t chunk = (span + n - 1) / n;
-  if (chunk < least) chunk = least;
   if (chunk > most) chunk = most;
+  if (chunk < least) chunk = least;
+  if (chunk < (span + most_splits - 1) / most_splits) chunk = (span + most_splits - 1) / most_splits;
   chunk = (chunk + 63) / 64 * 64;
   pl->chunk = (int)chunk;
-  // a range that does not start at a multiple of the chunk touches one more
-  pl->splits = (int)((span + chunk - 1) / chunk) + (p.window > 0 ? 1 : 0);
+  pl->splits = (int)((span + chunk - 1) / chunk);
+  if (pl->splits > 1 && p.window > 0) ++pl->splits;
   if (pl->splits < 1) pl->splits = 1;
+  // one chunk must hold the whole range wherever it starts
+  if (pl->splits == 1) pl->chunk = 1 << 30;
   pl->bytes = pl->splits > 1 ? align256((size_t)pl->splits * pl->part_rows * p.D * 4) +
                                    align256((size_t)pl->splits * pl->part_rows * 8)
                              : 0;
 }
 
-Plan plan_keys(const PagedAttn& p) {
+Plan plan_keys(int dtype, const PagedAttn& p) {
   Plan pl = {};
-  const int g = p.hq / p.hkv;
-  // one sequence with more rows than fit goes to attn_rows alone
-  pl.used = g <= kKeysRows && (p.n_seqs > 1 || (int64_t)p.max_q * g <= kKeysRows);
+  const int64_t g = p.hq / p.hkv, rows = p.max_q * g;
+  // a single sequence with more rows than fit goes to attn_rows alone
+  pl.used = p.n_seqs > 1 ? g <= kKeysMax : rows <= kKeysMax;
   if (!pl.used) return pl;
-  pl.tiles = p.n_seqs;
-  pl.part_rows = (size_t)p.n_seqs * p.hkv * kKeysRows;
-  split(&pl, p, key_span(p, kKeysRows / g), (int64_t)p.n_seqs * p.hkv, 4 * kCus, 256, 2048);
+  pl.max_rows = kKeysMax;
+  pl.tiles_per_seq = (int)(((rows < kKeysMax ? rows : kKeysMax) + kKeysTile - 1) / kKeysTile);
+  pl.tiles = p.n_seqs * pl.tiles_per_seq;
+  pl.part_rows = (size_t)pl.tiles * p.hkv * kKeysTile;
+  split(&pl, p, key_span(p, kKeysTile / g + 2), (int64_t)pl.tiles * p.hkv, 4 * kCus, 256, 2048);
   return pl;
 }
 
-Plan plan_rows(const PagedAttn& p, bool with_keys) {
+Plan plan_rows(int dtype, const PagedAttn& p, bool with_keys) {
   Plan pl = {};
-  const int g = p.hq / p.hkv;
-  pl.min_rows = with_keys ? kKeysRows : 0;
-  pl.used = (int64_t)p.max_q * g > pl.min_rows;
+  const int64_t g = p.hq / p.hkv;
+  pl.min_rows = with_keys ? kKeysMax : 0;
+  pl.used = p.max_q * g > pl.min_rows;
   if (!pl.used) return pl;
-  const int64_t rows = (int64_t)p.T * g;
+  const int64_t rows = p.T * g;
   // every taken sequence has at most one tile that is not full
   int64_t part = rows / (pl.min_rows + 1);
   if (part > p.n_seqs) part = p.n_seqs;
   pl.tiles = (int)(rows / kRowsTile + part);
   pl.part_rows = (size_t)pl.tiles * p.hkv * kRowsTile;
-  split(&pl, p, key_span(p, kRowsTile / g + 2), (int64_t)pl.tiles * p.hkv, 2 * kCus, 512, 1 << 30);
+  split(&pl, p, key_span(p, kRowsTile / g + 2), (int64_t)pl.tiles * p.hkv, 2 * kCus,
+        dtype == 1 ? 512 : 128, 1 << 30);
   return pl;
 }
 
 void place(AttnArgs* a, const Plan& pl, void* ws) {
   a->chunk = pl.chunk;
   a->min_rows = pl.min_rows;
+  a->max_rows = pl.max_rows;
+  a->tiles_per_seq = pl.tiles_per_seq;
   a->n_tiles = pl.tiles;
   a->part_rows = pl.part_rows;
   a->part_o = (float*)ws;
@@ -95,13 +107,12 @@ hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipS
   const bool fast = (p.D == 64 || p.D == 128 || p.D == 256) && p.page_size % 16 == 0 &&
                     p.kc_token < (1 << 24) && p.vc_token < (1 << 24);
   hipError_t e = hipSuccess;
-  const unsigned join_y = (unsigned)((p.D + 31) / 32);
   if (rows.used) {
     place(&a, rows, (char*)ws + keys.bytes);
     e = launch_attn_rows<T>(a, rows.splits, fast, s);
     if (e != hipSuccess) return e;
     if (rows.splits > 1) {
-      hipLaunchKernelGGL((attn_join<T, kRowsTile>), dim3((unsigned)(rows.tiles * p.hkv), join_y),
+      hipLaunchKernelGGL((attn_join<T, kRowsTile>), dim3((unsigned)(rows.tiles * p.hkv), 8),
                          dim3(256), 0, s, a);
       e = hipGetLastError();
       if (e != hipSuccess) return e;
@@ -112,7 +123,9 @@ hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipS
     e = launch_attn_keys<T>(a, keys.splits, fast, s);
     if (e != hipSuccess) return e;
     if (keys.splits > 1) {
-      hipLaunchKernelGGL((attn_join<T, kKeysRows>), dim3((unsigned)(p.n_seqs * p.hkv), 1), dim3(256),
+      const int64_t most = (int64_t)p.max_q * a.g < kKeysTile ? (int64_t)p.max_q * a.g : kKeysTile;
+      const unsigned join_y = (unsigned)((most + 3) / 4);  // a wave for every row
+      hipLaunchKernelGGL((attn_join<T, kKeysTile>), dim3((unsigned)(keys.tiles * p.hkv), join_y), dim3(256),
                          0, s, a);
       e = hipGetLastError();
     }
@@ -124,12 +137,12 @@ hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipS
 
 size_t paged_attn_workspace(int dtype, const PagedAttn& p) {
   if (p.T == 0 || p.n_seqs == 0 || p.max_q == 0) return 0;
-  const Plan keys = plan_keys(p);
-  return keys.bytes + plan_rows(p, keys.used).bytes;
+  const Plan keys = plan_keys(dtype, p);
+  return keys.bytes + plan_rows(dtype, p, keys.used).bytes;
 }
 
 hipError_t launch_paged_attn(int dtype, const PagedAttn& p, void* ws, hipStream_t stream) {
-  const Plan keys = plan_keys(p), rows = plan_rows(p, keys.used);
+  const Plan keys = plan_keys(dtype, p), rows = plan_rows(dtype, p, keys.used);
   AttnArgs a = {};
   a.p = p;
   a.g = p.hq / p.hkv;
