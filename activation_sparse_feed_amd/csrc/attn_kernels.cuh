@@ -131,7 +131,10 @@ template <typename T, int DP, int KT, int NW, bool FAST>
 __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void attn_rows(AttnArgs a) {
   typedef AttnTile<T, DP, KT> Tile;
   constexpr int TM = NW * 32;
-  extern __shared__ __align__(16) uint8_t lds[];
+  // separate arrays, and a loop unrolled over them: the compiler then knows that
+  // reads of one do not wait for the loads into another
+  __shared__ __align__(1024) uint8_t k0[Tile::kTileBytes], k1[Tile::kTileBytes], v0[Tile::kTileBytes],
+      v1[Tile::kTileBytes];
   const PagedAttn& p = a.p;
   // key heads run fastest over the workgroups, which go round the XCDs: with
   // eight of them (or a multiple) an XCD's L2 holds the keys of one head.  The
@@ -161,45 +164,70 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
   Tile tile;
   tile.init();
   tile.load_q((const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D, a.negate != 0);
-  if (p.D != DP || DP != Tile::kRowElems) {  // chunks that no load writes
-    for (int i = threadIdx.x; i < 4 * Tile::kTileBytes / 16; i += NW * 64)
-      ((u32x4_t*)lds)[i] = u32x4_t{0u, 0u, 0u, 0u};
+  if (p.D != DP) {  // chunks that are read, but that no load writes
+    for (int i = threadIdx.x * 16; i < Tile::kTileBytes; i += NW * 64 * 16)
+      *(u32x4_t*)(k0 + i) = *(u32x4_t*)(k1 + i) = *(u32x4_t*)(v0 + i) = *(u32x4_t*)(v1 + i) =
+          u32x4_t{0u, 0u, 0u, 0u};
     __syncthreads();
   }
   constexpr int kPer = Tile::kLoads / NW;
   static_assert(kPer >= 1, "");
-  TileLoader<T, DP, KT, FAST, kPer> loader;
-  loader.init(a, w.seq, hk, b, e, wave * kPer);
-  // keys that every row of the workgroup, of the wave sees
-  const int all_lo = x, all_hi = y;
-  int buf = 0, j0 = b & ~(KT - 1);
+  TileLoader<T, DP, KT, FAST, kPer, true> load_k;
+  TileLoader<T, DP, KT, FAST, kPer, false> load_v;
+  load_k.init(a, w.seq, hk, b, e, wave * kPer);
+  load_v.init(a, w.seq, hk, b, e, wave * kPer);
+  // The K tile that is in LDS beside a V tile is 32 keys ahead of it: step()
+  // needs the next block's K with a block's V.
+  f32x16_t s;
+  int j0 = b & ~(KT - 1);
   if (e > b) {
-    loader.look_up(j0);
-    loader.start(lds, lds + Tile::kTileBytes);
-    loader.look_up(j0 + KT);
-  }
-  for (; j0 < e; j0 += KT) {
+    load_k.look_up(j0 + 32 - KT);
+    load_v.look_up(j0);
+    load_k.start(k1);
+    load_k.look_up(j0 + 32);
+    load_v.start(v0);
+    load_v.look_up(j0 + KT);
+    load_k.start(k0);
+    load_k.look_up(j0 + KT + 32);
     wait_loads<0>();
-    __syncthreads();  // this tile is in LDS, and nobody reads the other one any more
-    uint8_t* k = lds + buf * 2 * Tile::kTileBytes;
-    uint8_t* v = k + Tile::kTileBytes;
+    __syncthreads();
+    s = tile.scores(k1 + KT * Tile::kPitch - Tile::kBlockBytes);
+  }
+  auto iteration = [&](uint8_t* k, uint8_t* v, uint8_t* k_next, uint8_t* v_next) __attribute__((always_inline)) {
+    wait_loads<0>();
+    __syncthreads();  // k and v are in LDS, and nobody reads the others any more
     if (j0 + KT < e) {
-      uint8_t* next = lds + (buf ^ 1) * 2 * Tile::kTileBytes;
-      loader.start(next, next + Tile::kTileBytes);
-      loader.look_up(j0 + 2 * KT);
+      load_v.start(v_next);
+      load_v.look_up(j0 + 2 * KT);
+      load_k.start(k_next);
+      load_k.look_up(j0 + 2 * KT + 32);
     }
-    if (!(j0 >= all_lo && j0 + KT <= all_hi) &&
+    if (!(j0 >= x && j0 + KT <= y) &&  // some row of the workgroup does not see some key
         __syncthreads_or(Tile::find_infinite(v, threadIdx.x, NW * 64))) {
       tile.add_infinite(v, j0, row_lo, row_hi);
       __syncthreads();
       Tile::clear_infinite(v, threadIdx.x, NW * 64);
       __syncthreads();
     }
-    if (wave_live && j0 < w_hi1 && j0 + KT > w_lo0)
-      tile.step(k, v, j0, row_lo, row_hi, j0 >= w_lo1 && j0 + KT <= w_hi0, a.c);
-    buf ^= 1;
+#pragma unroll
+    for (int i = 0; i < KT / 32; ++i) {
+      const int j = j0 + i * 32;
+      // the wave's rows see none of the block's keys, or not all of them
+      if (!wave_live || j >= w_hi1 || j + 32 <= w_lo0) {
+        s = tile.scores(k + i * Tile::kBlockBytes);
+      } else {
+        if (j < w_lo1 || j + 32 > w_hi0) Tile::hide(s, j, row_lo, row_hi);
+        tile.step(s, k + i * Tile::kBlockBytes, v + i * Tile::kBlockBytes, a.c);
+      }
+    }
+    j0 += KT;
+  };
+  while (j0 < e) {
+    iteration(k0, v0, k1, v1);
+    if (j0 >= e) break;
+    iteration(k1, v1, k0, v0);
   }
-  tile.l += other_half(tile.l);
+  tile.l = sum_halves(tile.l);
   const float m = tile.m * a.c;
   if (r0 + wave * 32 + (lane & 31) > r1) return;
   if (n_split == 1) {
@@ -239,7 +267,9 @@ template <typename T, int DP, int NW, bool FAST>
 __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
   constexpr int KT = 32;
   typedef AttnTile<T, DP, KT> Tile;
-  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ __align__(1024) uint8_t k0[NW][Tile::kTileBytes], k1[NW][Tile::kTileBytes],
+      v0[NW][Tile::kTileBytes], v1[NW][Tile::kTileBytes];
+  __shared__ float ml[NW][32][2];
   const PagedAttn& p = a.p;
   const int hk = (int)blockIdx.x % p.hkv, split = blockIdx.y, t = (int)blockIdx.x / p.hkv;
   const Work w = sequence_tile(a, t);
@@ -258,54 +288,68 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
   Tile tile;
   tile.init();
   tile.load_q((const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D, a.negate != 0);
-  uint8_t* mine = lds + wave * 4 * Tile::kTileBytes;
-  if (p.D != DP || DP != Tile::kRowElems)
-    for (int i = lane; i < 4 * Tile::kTileBytes / 16; i += kWave)
-      ((u32x4_t*)mine)[i] = u32x4_t{0u, 0u, 0u, 0u};
-  TileLoader<T, DP, KT, FAST, Tile::kLoads> loader;
-  loader.init(a, w.seq, hk, b, e, 0);
-  int buf = 0, j0 = (b & ~(KT - 1)) + wave * KT;
+  if (p.D != DP)  // chunks that are read, but that no load writes
+    for (int i = lane * 16; i < Tile::kTileBytes; i += kWave * 16)
+      *(u32x4_t*)(k0[wave] + i) = *(u32x4_t*)(k1[wave] + i) = *(u32x4_t*)(v0[wave] + i) =
+          *(u32x4_t*)(v1[wave] + i) = u32x4_t{0u, 0u, 0u, 0u};
+  TileLoader<T, DP, KT, FAST, Tile::kLoads, true> load_k;
+  TileLoader<T, DP, KT, FAST, Tile::kLoads, false> load_v;
+  load_k.init(a, w.seq, hk, b, e, 0);
+  load_v.init(a, w.seq, hk, b, e, 0);
+  int j0 = (b & ~(KT - 1)) + wave * KT;
   __builtin_amdgcn_s_waitcnt(0xC07F);  // the zeros are written (lgkmcnt)
   if (j0 < e) {
-    loader.look_up(j0);
-    loader.start(mine, mine + Tile::kTileBytes);
-    loader.look_up(j0 + NW * KT);
+    load_k.look_up(j0);
+    load_v.look_up(j0);
+    load_k.start(k0[wave]);
+    load_v.start(v0[wave]);
+    load_k.look_up(j0 + NW * KT);
+    load_v.look_up(j0 + NW * KT);
   }
-  for (; j0 < e; j0 += NW * KT) {
+  auto iteration = [&](uint8_t* k, uint8_t* v, uint8_t* k_next, uint8_t* v_next) __attribute__((always_inline)) {
     wait_loads<0>();
-    uint8_t* k = mine + buf * 2 * Tile::kTileBytes;
-    uint8_t* v = k + Tile::kTileBytes;
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     if (j0 + NW * KT < e) {
-      uint8_t* next = mine + (buf ^ 1) * 2 * Tile::kTileBytes;
-      loader.start(next, next + Tile::kTileBytes);
-      loader.look_up(j0 + 2 * NW * KT);
+      load_k.start(k_next);
+      load_v.start(v_next);
+      load_k.look_up(j0 + 2 * NW * KT);
+      load_v.look_up(j0 + 2 * NW * KT);
     }
     const bool whole = j0 >= x && j0 + KT <= y;
     if (!whole && __any(Tile::find_infinite(v, lane, kWave))) {
       tile.add_infinite(v, j0, row_lo, row_hi);
       Tile::clear_infinite(v, lane, kWave);
     }
-    tile.step(k, v, j0, row_lo, row_hi, whole, a.c);
-    buf ^= 1;
+    f32x16_t s = tile.scores(k);
+    if (!whole) Tile::hide(s, j0, row_lo, row_hi);
+    tile.raise(s, a.c);
+    tile.weights(s, a.c);
+    tile.accumulate(v, s);
+    j0 += NW * KT;
+  };
+  while (j0 < e) {
+    iteration(k0[wave], v0[wave], k1[wave], v1[wave]);
+    if (j0 >= e) break;
+    iteration(k1[wave], v1[wave], k0[wave], v0[wave]);
   }
-  tile.l += other_half(tile.l);
-  // join the waves: each leaves its rows in LDS, [row][d] with a pitch that keeps
-  // 16-byte writes of neighbouring rows apart
-  constexpr int kPitchO = DP + 4;
-  __syncthreads();
-  float* po = (float*)lds;  // [NW][32][kPitchO], then [NW][32][2]
-  float* pm = po + NW * 32 * kPitchO;
+  tile.l = sum_halves(tile.l);
+  // Join the waves: each leaves its rows in its K arrays, 32 x 32 floats for each
+  // block of 32 outputs, row r's 16-byte chunk c at c ^ (r % 8).
+  constexpr int kPerArray = Tile::kTileBytes / 4096;
+  static_assert(kPerArray * 2 >= Tile::kDt, "");
+  auto part = [&](int wv, int d) { return (d < kPerArray ? k0[wv] + d * 4096 : k1[wv] + (d - kPerArray) * 4096); };
   {
-    float* row = po + (wave * 32 + (lane & 31)) * kPitchO;
+    const int row = lane & 31;
 #pragma unroll
     for (int d = 0; d < Tile::kDt; ++d)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        store4<float>(row + d * 32 + 8 * i + 4 * half, tile.o[d][4 * i], tile.o[d][4 * i + 1],
-                      tile.o[d][4 * i + 2], tile.o[d][4 * i + 3]);
+        store4<float>((float*)(part(wave, d) + row * 128 + (((2 * i + half) ^ (row & 7)) << 4)),
+                      tile.o[d][4 * i], tile.o[d][4 * i + 1], tile.o[d][4 * i + 2], tile.o[d][4 * i + 3]);
     if (half == 0) {
-      pm[(wave * 32 + (lane & 31)) * 2] = tile.m * a.c;
-      pm[(wave * 32 + (lane & 31)) * 2 + 1] = tile.l;
+      ml[wave][row][0] = tile.m * a.c;
+      ml[wave][row][1] = tile.l;
     }
   }
   __syncthreads();
@@ -314,14 +358,15 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
     const int rr = i / quads, d = (i - rr * quads) * 4;
     float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int k = 0; k < NW; ++k) m = fmaxf(m, pm[(k * 32 + rr) * 2]);
+    for (int k = 0; k < NW; ++k) m = fmaxf(m, ml[k][rr][0]);
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < NW; ++k) {
-      const float mk = pm[(k * 32 + rr) * 2];
+      const float mk = ml[k][rr][0];
       const float f = mk == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mk - m);
-      l += f * pm[(k * 32 + rr) * 2 + 1];
-      if (mk != -INFINITY) v += f * *(const f32x4_t*)(po + (k * 32 + rr) * kPitchO + d);
+      l += f * ml[k][rr][1];
+      if (mk != -INFINITY)
+        v += f * *(const f32x4_t*)(part(k, d / 32) + rr * 128 + (((d % 32 / 4) ^ (rr & 7)) << 4));
     }
     const int tk = a.group.div(r0 + rr), hd = hk * a.g + r0 + rr - tk * a.g;
     if (n_split == 1) {
@@ -396,17 +441,13 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
 template <typename T> hipError_t launch_attn_rows(const AttnArgs& a, int splits, bool fast, hipStream_t s);
 template <typename T> hipError_t launch_attn_keys(const AttnArgs& a, int splits, bool fast, hipStream_t s);
 
-// Key tile and waves of attn_rows, waves of attn_keys, and the bytes of LDS.
+// Key tile and waves of attn_rows, waves of attn_keys.
 template <typename T, int DP> struct RowsShape {
   static constexpr int kWaves = 4;
   static constexpr int kKeys = sizeof(T) == 2 && DP <= 128 ? 64 : 32;
-  static constexpr size_t kLds = 4 * (size_t)AttnTile<T, DP, kKeys>::kTileBytes;
 };
 template <typename T, int DP> struct KeysShape {
   static constexpr int kWaves = sizeof(T) == 4 && DP > 128 ? 1 : 2;
-  static constexpr size_t kTiles = kWaves * 4 * (size_t)AttnTile<T, DP, 32>::kTileBytes;
-  static constexpr size_t kJoin = (size_t)kWaves * 32 * (DP + 4 + 2) * 4;
-  static constexpr size_t kLds = kTiles > kJoin ? kTiles : kJoin;
 };
 
 #define SFFN_ATTN_BY_WIDTH(F, T, ...)                  \
@@ -425,10 +466,10 @@ hipError_t attn_rows_width(const AttnArgs& a, int splits, bool fast, hipStream_t
   const dim3 grid((unsigned)(a.n_tiles * a.p.hkv), (unsigned)splits);
   if (fast)
     hipLaunchKernelGGL((attn_rows<T, DP, S::kKeys, S::kWaves, true>), grid, dim3(S::kWaves * 64),
-                       S::kLds, s, a);
+                       0, s, a);
   else
     hipLaunchKernelGGL((attn_rows<T, DP, S::kKeys, S::kWaves, false>), grid, dim3(S::kWaves * 64),
-                       S::kLds, s, a);
+                       0, s, a);
   return hipGetLastError();
 }
 
@@ -437,9 +478,9 @@ hipError_t attn_keys_width(const AttnArgs& a, int splits, bool fast, hipStream_t
   typedef KeysShape<T, DP> S;
   const dim3 grid((unsigned)(a.n_tiles * a.p.hkv), (unsigned)splits);
   if (fast)
-    hipLaunchKernelGGL((attn_keys<T, DP, S::kWaves, true>), grid, dim3(S::kWaves * 64), S::kLds, s, a);
+    hipLaunchKernelGGL((attn_keys<T, DP, S::kWaves, true>), grid, dim3(S::kWaves * 64), 0, s, a);
   else
-    hipLaunchKernelGGL((attn_keys<T, DP, S::kWaves, false>), grid, dim3(S::kWaves * 64), S::kLds, s, a);
+    hipLaunchKernelGGL((attn_keys<T, DP, S::kWaves, false>), grid, dim3(S::kWaves * 64), 0, s, a);
   return hipGetLastError();
 }
 

@@ -93,12 +93,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// Maximum / sum with the other half of the wave (lane ^ 32).
-__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, kWave); }
+// The value of lane ^ 32 is in one of the two results of the swap, the lane's own in
+// the other.
+__device__ __forceinline__ float max_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
 
 // ------------------------------------------------------------------ the tile
 // T: uint16_t (bf16) or float; DP: head_dim rounded up to the instances below;
-// KT: keys of an LDS tile (a multiple of 32).
+// KT: keys of an LDS tile, 32 or 64: K and V tiles are walked over in blocks of 32.
 template <typename T, int DP, int KT>
 struct AttnTile {
   static constexpr int kEpc = 16 / (int)sizeof(T);         // elements of a 16-byte chunk
@@ -107,15 +115,15 @@ struct AttnTile {
   static constexpr int kCpr = kPitch / 16;                 // chunks of a row
   static constexpr int kRpi = kWave / kCpr;                // rows of one wave-wide load
   static constexpr int kLoads = KT / kRpi;                 // wave-wide loads of a K or V tile
-  static constexpr int kKeyBlocks = KT / 32;
   static constexpr int kQ = DP / (2 * kEpc);               // Q and K fragments of a row
   static constexpr int kDt = DP / 32;                      // 32-wide blocks of the output
   static constexpr int kTileBytes = KT * kPitch;           // of K, and again of V
+  static constexpr int kBlockBytes = 32 * kPitch;
   static_assert(kRpi >= 1 && KT % 32 == 0 && DP % 32 == 0, "");
 
   // Chunk permutation of row r.  K is read by 32 rows at one chunk: any 16
   // neighbouring rows get 16 different chunks (8 when a row has 8).  V is read
-  // as 64 bytes of 8 neighbouring rows.
+  // as 64 bytes of 8 neighbouring rows.  No bank conflicts are counted.
   __device__ static __forceinline__ int swz_k(int r) { return r & (kCpr < 16 ? kCpr - 1 : 15); }
   __device__ static __forceinline__ int swz_v(int r) {
     if constexpr (sizeof(T) == 4) return 0;  // read row by row: no conflicts
@@ -147,36 +155,43 @@ struct AttnTile {
     }
   }
 
-  // S^T of key block kb of the K tile at `k`.
-  __device__ __forceinline__ f32x16_t scores(const uint8_t* k, int kb) const {
+  // S^T of the 32 keys at `k`.
+  __device__ __forceinline__ f32x16_t scores(const uint8_t* k) const {
     const int lane = lane_id(), r = lane & 31, h = lane >> 5;
-    const uint8_t* row = k + (kb * 32 + r) * kPitch;
+    const int at = r * kPitch + ((h ^ swz_k(r)) << 4);
+    u32x4_t a[kQ];
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) a[i] = *(const u32x4_t*)(k + (at ^ (i << 5)));
     f32x16_t s;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
-    for (int i = 0; i < kQ; ++i) {
-      const u32x4_t a = *(const u32x4_t*)(row + (((2 * i + h) ^ swz_k(r)) << 4));
-      s = Frag<T>::mma(a, q[i], s);
-    }
+    for (int i = 0; i < kQ; ++i) s = Frag<T>::mma(a[i], q[i], s);
     return s;
   }
 
-  // Index within a key block of a lane's S^T value i.
+  // Index within a block of a lane's S^T value i.
   __device__ static __forceinline__ int key_of(int i, int half) { return 8 * (i >> 2) + 4 * half + (i & 3); }
 
-  // Softmax step over the tile's scores: s becomes the weights.  The maximum
-  // is only moved (and l and o scaled) when it grows by more than 2^8 in some
-  // row: weights up to 2^8 keep their relative precision in any type, and most
-  // tiles then leave o alone.
-  __device__ __forceinline__ void softmax(f32x16_t (&s)[kKeyBlocks], float c) {
-    float mx = s[0][0];
+  // Scores of keys that the row does not see (it sees lo .. hi - 1) become -inf; j:
+  // the block's first key.
+  __device__ static __forceinline__ void hide(f32x16_t& s, int j, int lo, int hi) {
+    const int h = lane_id() >> 5;
 #pragma unroll
-    for (int b = 0; b < kKeyBlocks; ++b)
+    for (int i = 0; i < 16; ++i) {
+      const int k = j + key_of(i, h);
+      s[i] = k >= lo && k < hi ? s[i] : -INFINITY;
+    }
+  }
+
+  // Moves the running maximum to that of the scores (and scales l and o) where
+  // some row's grows by more than a factor of 2^8: weights up to 2^8 keep their
+  // relative precision in any type, and most blocks then leave o alone.
+  __device__ __forceinline__ void raise(const f32x16_t& s, float c) {
+    float mx = s[0];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
-    mx = fmaxf(mx, other_half(mx));
-    const float mn = fmaxf(m, mx);
+    for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
+    const float mn = fmaxf(m, max_halves(mx));
     if (__any((mn - m) * c > 8.f)) {
       const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * c);
       l *= f;
@@ -186,59 +201,66 @@ struct AttnTile {
         for (int i = 0; i < 16; ++i) o[d][i] *= f;
       m = mn;
     }
+  }
+
+  // s becomes the weights, their sum is added to l.
+  __device__ __forceinline__ void weights(f32x16_t& s, float c) {
     const float mc = m == -INFINITY ? 0.f : m * c;
     float sum = 0.f;
 #pragma unroll
-    for (int b = 0; b < kKeyBlocks; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], c, -mc));
-        s[b][i] = w;
-        sum += w;
-      }
+    for (int i = 0; i < 16; ++i) {
+      s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -mc));
+      sum += s[i];
+    }
     l += sum;
   }
 
-  // V^T fragment (A operand): rows (d) dt * 32 + lane % 32, the 16 keys of step
-  // ks in the order of the weights.  Two transposing reads: 16 lanes read 4 keys
-  // x 16 elements and each gets one element of the 4 keys.
+  // V^T fragment (A operand) of the 32 keys at v: rows (d) dt * 32 + lane % 32, the
+  // 16 keys of half ks in the order of the weights.  Two transposing reads: 16
+  // lanes read 4 keys x 16 elements and each gets one element of the 4 keys.
   __device__ static __forceinline__ u32x4_t v_frag(const uint8_t* v, int ks, int dt) {
     const int lane = lane_id(), i = lane & 15, g = lane >> 4;
-    const int r = ks * 16 + 4 * (g >> 1) + (i >> 2);
-    const int c = dt * 4 + 2 * (g & 1) + ((i & 3) >> 1);
-    const uint8_t* a0 = v + r * kPitch + ((c ^ swz_v(r)) << 4) + (i & 1) * 8;
-    const uint8_t* a1 = v + (r + 8) * kPitch + ((c ^ swz_v(r + 8)) << 4) + (i & 1) * 8;
-    const s16x4_t x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)a0);
-    const s16x4_t x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)a1);
-    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    const int r = 4 * (g >> 1) + (i >> 2);  // swz_v(r + 8) is swz_v(r)
+    const int c = (2 * (g & 1) + ((i & 3) >> 1)) ^ swz_v(r);
+    const uint8_t* a = v + ks * 16 * kPitch + ((r * kPitch + (c << 4) + (i & 1) * 8) ^ (dt << 6));
+    typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+    const s16x4_t x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)a);
+    const s16x4_t x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(a + 8 * kPitch));
     return __builtin_bit_cast(u32x4_t, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
   }
 
-  // o += V^T P^T.
-  __device__ __forceinline__ void accumulate(const uint8_t* v, const f32x16_t (&s)[kKeyBlocks]) {
+  // o += V^T P^T over the 32 keys at v.
+  __device__ __forceinline__ void accumulate(const uint8_t* v, const f32x16_t& s) {
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int ks = 0; ks < KT / 16; ++ks) {
-        u32x4_t pf;
+      for (int ks = 0; ks < 2; ++ks) {
+        u32x4_t pf;  // the weights are rounded to the type of V here
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          pf[j] = pack_bf16(s[ks / 2][8 * (ks & 1) + 2 * j], s[ks / 2][8 * (ks & 1) + 2 * j + 1]);
+        for (int j = 0; j < 4; ++j) pf[j] = pack_bf16(s[8 * ks + 2 * j], s[8 * ks + 2 * j + 1]);
 #pragma unroll
         for (int d = 0; d < kDt; ++d) o[d] = Frag<T>::mma(v_frag(v, ks, d), pf, o[d]);
       }
     } else {
-      const int r0 = 4 * (lane_id() >> 5), col = lane_id() & 31;
+      const uint8_t* at = v + 4 * (lane_id() >> 5) * kPitch + (lane_id() & 31) * 4;
 #pragma unroll
-      for (int b = 0; b < kKeyBlocks; ++b)
+      for (int i = 0; i < 16; ++i)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-#pragma unroll
-          for (int d = 0; d < kDt; ++d) {
-            const float x = *(const float*)(v + (b * 32 + 8 * (i >> 2) + (i & 3) + r0) * kPitch +
-                                            (d * 32 + col) * 4);
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, s[b][i], o[d], 0, 0, 0);
-          }
+        for (int d = 0; d < kDt; ++d) {
+          const float x = *(const float*)(at + (8 * (i >> 2) + (i & 3)) * kPitch + d * 128);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, s[i], o[d], 0, 0, 0);
+        }
     }
+  }
+
+  // One block of 32 keys whose scores are in s, and the scores of the next one: its
+  // matrix instructions do not depend on this block's exponentials, so a wave has
+  // both to issue side by side.
+  __device__ __forceinline__ void step(f32x16_t& s, const uint8_t* k_next, const uint8_t* v, float c) {
+    raise(s, c);
+    const f32x16_t next = scores(k_next);
+    weights(s, c);
+    accumulate(v, s);
+    s = next;
   }
 
   // A key that a row does not see has weight 0, but 0 times an infinite or NaN
@@ -274,6 +296,7 @@ struct AttnTile {
       *(u32x4_t*)(v + at) = x;
     }
   }
+  // j0: the tile's first key.
   __device__ __forceinline__ void add_infinite(const uint8_t* v, int j0, int lo, int hi) {
     const int h = lane_id() >> 5;
 #pragma unroll 1
@@ -290,30 +313,6 @@ struct AttnTile {
         }
     }
   }
-
-  // Scores of keys that the row does not see (it sees lo .. hi - 1) become -inf.
-  __device__ static __forceinline__ void hide(f32x16_t (&s)[kKeyBlocks], int j0, int lo, int hi) {
-    const int h = lane_id() >> 5;
-#pragma unroll
-    for (int b = 0; b < kKeyBlocks; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int j = j0 + b * 32 + key_of(i, h);
-        s[b][i] = j >= lo && j < hi ? s[b][i] : -INFINITY;
-      }
-  }
-
-  // One tile that starts at key j0: scores, softmax, product with V.  whole: every
-  // row of the wave sees every key.
-  __device__ __forceinline__ void step(const uint8_t* k, const uint8_t* v, int j0, int lo, int hi,
-                                       bool whole, float c) {
-    f32x16_t s[kKeyBlocks];
-#pragma unroll
-    for (int b = 0; b < kKeyBlocks; ++b) s[b] = scores(k, b);
-    if (!whole) hide(s, j0, lo, hi);
-    softmax(s, c);
-    accumulate(v, s);
-  }
 };
 
 // ------------------------------------------------------------------ the loads
@@ -328,34 +327,32 @@ __device__ __forceinline__ int load_uniform(const int32_t* p) {
   return *(const __attribute__((address_space(4))) int32_t*)p;
 }
 
-// Copies key rows to LDS, N wave-wide loads per tile.  FAST: the rows of a granule
-// of G lie in one page (page_size a multiple of 16) and fill their LDS rows
-// (head_dim == kRowElems), so a page is looked up once a granule with scalar
-// instructions and a lane only adds a constant offset; otherwise every lane
-// looks up its own rows.  Pages are looked up one tile ahead.
-template <typename T, int DP, int KT, bool FAST, int N>
+// Copies the key rows of one cache (K or V) to LDS, N wave-wide loads per tile and
+// wave.  FAST: the rows of a granule of kG lie in one page (page_size a multiple of
+// 16) and fill their LDS rows (head_dim == kRowElems), so a page is looked up once a
+// granule with scalar instructions and a lane only adds a constant offset; otherwise
+// every lane looks up its own rows.  Pages are looked up one tile ahead.
+template <typename T, int DP, int KT, bool FAST, int N, bool K>
 struct TileLoader {
   typedef AttnTile<T, DP, KT> Tile;
+  static constexpr int kG = !FAST ? Tile::kRpi : N * Tile::kRpi < 16 ? N * Tile::kRpi : 16;
+  static constexpr int kPerG = kG / Tile::kRpi;  // wave-wide loads of a granule
   const int32_t* bt;
-  const uint8_t *k, *v;         // of the key head
-  uint64_t k_page, v_page;      // bytes
-  int64_t k_token, v_token;
+  const uint8_t* base;          // of the key head
+  uint64_t page_bytes;
+  int64_t token_bytes;
   FastDiv per_page;
   int last_page, first, last;   // keys that exist for this tile: the others repeat one of them
   int i0, n_chunks;             // this wave's first wave-wide load of a tile; chunks of a row
-  static constexpr int kG = !FAST ? Tile::kRpi : N * Tile::kRpi < 16 ? N * Tile::kRpi : 16;
-  static constexpr int kPerG = kG / Tile::kRpi;  // wave-wide loads of a granule
-  int page[N / kPerG], off[N / kPerG];           // of the next tile
+  int page[N / kPerG], off[N / kPerG];  // of the next tile
 
   __device__ __forceinline__ void init(const AttnArgs& a, int seq, int hk, int lo, int hi, int load0) {
     const PagedAttn& p = a.p;
     bt = p.block_table + (size_t)seq * p.max_pages;
-    k = (const uint8_t*)((const T*)p.k_cache + hk * p.kc_head);
-    v = (const uint8_t*)((const T*)p.v_cache + hk * p.vc_head);
-    k_page = (uint64_t)p.kc_page * sizeof(T);
-    v_page = (uint64_t)p.vc_page * sizeof(T);
-    k_token = p.kc_token * (int64_t)sizeof(T);
-    v_token = p.vc_token * (int64_t)sizeof(T);
+    base = K ? (const uint8_t*)((const T*)p.k_cache + hk * p.kc_head)
+             : (const uint8_t*)((const T*)p.v_cache + hk * p.vc_head);
+    page_bytes = (uint64_t)(K ? p.kc_page : p.vc_page) * sizeof(T);
+    token_bytes = (K ? p.kc_token : p.vc_token) * (int64_t)sizeof(T);
     per_page = a.page;
     last_page = p.n_pages - 1;
     first = lo, last = hi - 1;
@@ -363,6 +360,7 @@ struct TileLoader {
     n_chunks = p.D / Tile::kEpc;
   }
 
+  // The tile of the keys j0 .. j0 + KT - 1 (j0 a multiple of 32).
   __device__ __forceinline__ void look_up(int j0) {
 #pragma unroll
     for (int n = 0; n < N / kPerG; ++n) {
@@ -377,26 +375,21 @@ struct TileLoader {
   }
 
   // Starts the loads of the tile that was looked up.
-  __device__ __forceinline__ void start(uint8_t* k_tile, uint8_t* v_tile) const {
+  __device__ __forceinline__ void start(uint8_t* tile) const {
     const int rin = lane_id() / Tile::kCpr, chunk = lane_id() % Tile::kCpr;
 #pragma unroll
     for (int g = 0; g < N / kPerG; ++g) {
       const uint32_t pg = (uint32_t)min(max(page[g], 0), last_page);
-      const uint8_t* kr = k + (pg * k_page + off[g] * k_token);
-      const uint8_t* vr = v + (pg * v_page + off[g] * v_token);
+      const uint8_t* row = base + (pg * page_bytes + off[g] * token_bytes);
 #pragma unroll
       for (int m = 0; m < kPerG; ++m) {
         const int i = i0 + g * kPerG + m, r = i * Tile::kRpi + rin;
-        const int ck = chunk ^ Tile::swz_k(r), cv = chunk ^ Tile::swz_v(r);
-        uint8_t* kd = k_tile + i * 1024;
-        uint8_t* vd = v_tile + i * 1024;
-        if constexpr (FAST) {
-          copy16(kr + m * Tile::kRpi * k_token + ((uint32_t)rin * (uint32_t)k_token + ck * 16), kd);
-          copy16(vr + m * Tile::kRpi * v_token + ((uint32_t)rin * (uint32_t)v_token + cv * 16), vd);
-        } else {
-          if (ck < n_chunks) copy16(kr + ck * 16, kd);
-          if (cv < n_chunks) copy16(vr + cv * 16, vd);
-        }
+        const int c = chunk ^ (K ? Tile::swz_k(r) : Tile::swz_v(r));
+        uint8_t* to = tile + i * 1024;
+        if constexpr (FAST)
+          copy16(row + m * Tile::kRpi * token_bytes + ((uint32_t)rin * (uint32_t)token_bytes + c * 16), to);
+        else if (c < n_chunks)
+          copy16(row + c * 16, to);
       }
     }
   }
