@@ -27,50 +27,51 @@ struct Work {
 };
 
 __device__ __forceinline__ void read_sequence(const PagedAttn& p, int s, Work* w) {
-  const int a = min(max(p.q_start[s], 0), p.T), b = min(max(p.q_start[s + 1], a), p.T);
+  s = uniform(s);
+  const int q0 = load_uniform(p.q_start + s), q1 = load_uniform(p.q_start + s + 1);
+  const int len = load_uniform(p.kv_len + s);
+  const int a = min(max(q0, 0), p.T), b = min(max(q1, a), p.T);
   w->seq = s;
   w->q0 = a;
   w->nq = b - a;
-  w->nkv = min(max(p.kv_len[s], 0), p.max_kv);
+  w->nkv = min(max(len, 0), p.max_kv);
 }
 
-// Row tile number `t` of the sequences with more than min_rows rows, in order:
-// 64 sequences a step, a prefix sum of their tiles.
+// Row tile number `t` of the sequences with more than min_rows rows.  Among 64
+// neighbouring sequences the longest come first, and of a sequence the last rows,
+// which see most keys: tiles start in order of their work, so that the last ones
+// to end are short.  `t` runs over the tiles of 64 sequences in that order.
 template <int TM>
 __device__ __forceinline__ Work find_tile(const AttnArgs& a, int t) {
   const PagedAttn& p = a.p;
   Work w;
   w.tile = -1;
   w.seq = w.q0 = w.nq = w.nkv = 0;
-  int base = 0;
   for (int s0 = 0; s0 < p.n_seqs; s0 += kWave) {
     const int s = s0 + lane_id();
-    int n = 0;
+    int n = 0, len = -1;
     if (s < p.n_seqs) {
       const int b = min(max(p.q_start[s], 0), p.T), e = min(max(p.q_start[s + 1], b), p.T);
       const int rows = (e - b) * a.g;
       n = rows > a.min_rows ? (rows + TM - 1) / TM : 0;
+      len = p.kv_len[s];
     }
-    int up = n;  // inclusive prefix sum
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-      const int v = __shfl_up(up, o, kWave);
-      if (lane_id() >= o) up += v;
+    // tiles of the sequences before this one, and of all
+    int before = 0, all = 0;
+    for (int k = 0; k < min(p.n_seqs - s0, kWave); ++k) {
+      const int nk = __builtin_amdgcn_readlane(n, k), lk = __builtin_amdgcn_readlane(len, k);
+      all += nk;
+      before += lk > len || (lk == len && k < lane_id()) ? nk : 0;
     }
-    const uint64_t hit = __ballot(base + up > t);
+    const uint64_t hit = __ballot(t >= before && t < before + n);
     if (hit != 0) {
       const int k = (int)__builtin_ctzll(hit);
       read_sequence(p, s0 + k, &w);
-      w.tile = t - (base + __shfl(up - n, k, kWave));
+      w.tile = __builtin_amdgcn_readlane(n, k) - 1 - (t - __builtin_amdgcn_readlane(before, k));
       break;
     }
-    base += __shfl(up, kWave - 1, kWave);
+    t -= all;
   }
-  w.seq = uniform(w.seq);
-  w.q0 = uniform(w.q0);
-  w.nq = uniform(w.nq);
-  w.nkv = uniform(w.nkv);
-  w.tile = uniform(w.tile);
   return w;
 }
 
@@ -137,9 +138,8 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
       v1[Tile::kTileBytes];
   const PagedAttn& p = a.p;
   // key heads run fastest over the workgroups, which go round the XCDs: with
-  // eight of them (or a multiple) an XCD's L2 holds the keys of one head.  The
-  // last tiles, which see most keys, start first.
-  const int hk = (int)blockIdx.x % p.hkv, t = a.n_tiles - 1 - (int)blockIdx.x / p.hkv;
+  // eight of them (or a multiple) an XCD's L2 holds the keys of one head.
+  const int hk = (int)blockIdx.x % p.hkv, t = (int)blockIdx.x / p.hkv;
   const int split = blockIdx.y;
   const Work w = find_tile<TM>(a, t);
   if (w.tile < 0) return;
@@ -163,7 +163,6 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
 
   Tile tile;
   tile.init();
-  tile.load_q((const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D, a.negate != 0);
   if (p.D != DP) {  // chunks that are read, but that no load writes
     for (int i = threadIdx.x * 16; i < Tile::kTileBytes; i += NW * 64 * 16)
       *(u32x4_t*)(k0 + i) = *(u32x4_t*)(k1 + i) = *(u32x4_t*)(v0 + i) = *(u32x4_t*)(v1 + i) =
@@ -176,6 +175,7 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
   TileLoader<T, DP, KT, FAST, kPer, false> load_v;
   load_k.init(a, w.seq, hk, b, e, wave * kPer);
   load_v.init(a, w.seq, hk, b, e, wave * kPer);
+  const T* q = (const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head;
   // The K tile that is in LDS beside a V tile is 32 keys ahead of it: step()
   // needs the next block's K with a block's V.
   f32x16_t s;
@@ -189,6 +189,7 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
     load_v.look_up(j0 + KT);
     load_k.start(k0);
     load_k.look_up(j0 + KT + 32);
+    tile.load_q(q, p.D, a.negate != 0);
     wait_loads<0>();
     __syncthreads();
     s = tile.scores(k1 + KT * Tile::kPitch - Tile::kBlockBytes);
@@ -203,10 +204,10 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
       load_k.look_up(j0 + 2 * KT + 32);
     }
     if (!(j0 >= x && j0 + KT <= y) &&  // some row of the workgroup does not see some key
-        __syncthreads_or(Tile::find_infinite(v, threadIdx.x, NW * 64))) {
+        __syncthreads_or(Tile::template find_infinite<NW * 64>(v, threadIdx.x))) {
       tile.add_infinite(v, j0, row_lo, row_hi);
       __syncthreads();
-      Tile::clear_infinite(v, threadIdx.x, NW * 64);
+      Tile::template clear_infinite<NW * 64>(v, threadIdx.x);
       __syncthreads();
     }
 #pragma unroll
@@ -287,7 +288,6 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
   key_range(p, w, token, &row_lo, &row_hi);
   Tile tile;
   tile.init();
-  tile.load_q((const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D, a.negate != 0);
   if (p.D != DP)  // chunks that are read, but that no load writes
     for (int i = lane * 16; i < Tile::kTileBytes; i += kWave * 16)
       *(u32x4_t*)(k0[wave] + i) = *(u32x4_t*)(k1[wave] + i) = *(u32x4_t*)(v0[wave] + i) =
@@ -298,28 +298,27 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
   load_v.init(a, w.seq, hk, b, e, 0);
   int j0 = (b & ~(KT - 1)) + wave * KT;
   __builtin_amdgcn_s_waitcnt(0xC07F);  // the zeros are written (lgkmcnt)
+  auto load = [&](int j, uint8_t* k, uint8_t* v) __attribute__((always_inline)) {
+    load_k.start(k);
+    load_v.start(v);
+    load_k.look_up(j + NW * KT);
+    load_v.look_up(j + NW * KT);
+  };
   if (j0 < e) {
     load_k.look_up(j0);
     load_v.look_up(j0);
-    load_k.start(k0[wave]);
-    load_v.start(v0[wave]);
-    load_k.look_up(j0 + NW * KT);
-    load_v.look_up(j0 + NW * KT);
+    load(j0, k0[wave], v0[wave]);
+    tile.load_q((const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D, a.negate != 0);
   }
   auto iteration = [&](uint8_t* k, uint8_t* v, uint8_t* k_next, uint8_t* v_next) __attribute__((always_inline)) {
     wait_loads<0>();
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    if (j0 + NW * KT < e) {
-      load_k.start(k_next);
-      load_v.start(v_next);
-      load_k.look_up(j0 + 2 * NW * KT);
-      load_v.look_up(j0 + 2 * NW * KT);
-    }
+    if (j0 + NW * KT < e) load(j0 + NW * KT, k_next, v_next);
     const bool whole = j0 >= x && j0 + KT <= y;
-    if (!whole && __any(Tile::find_infinite(v, lane, kWave))) {
+    if (!whole && __any(Tile::template find_infinite<kWave>(v, lane))) {
       tile.add_infinite(v, j0, row_lo, row_hi);
-      Tile::clear_infinite(v, lane, kWave);
+      Tile::template clear_infinite<kWave>(v, lane);
     }
     f32x16_t s = tile.scores(k);
     if (!whole) Tile::hide(s, j0, row_lo, row_hi);
@@ -418,11 +417,16 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
     const float f = ms == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms - m);
     const float l = wave_sum(f * ls);
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-    const float* o = a.part_o + slot * p.D + d;
-#pragma unroll 4
-    for (int s = sub; s - sub < n; s += side) {
-      const float fs = __shfl(f, s & (kWave - 1), kWave);
-      if (s < n && fs != 0.f && d < p.D) v += fs * *(const f32x4_t*)(o + (size_t)s * a.part_rows * p.D);
+    const float* o = a.part_o + slot * p.D + (d < p.D ? d : 0);
+    // loads without conditions, so that they are in flight together: a split past the
+    // last one repeats it with a factor of 0
+#pragma unroll 8
+    for (int s0 = 0; s0 < n; s0 += side) {
+      const int s = s0 + sub, sc = min(s, n - 1);
+      const float fc = __shfl(f, sc, kWave), fs = s < n ? fc : 0.f;
+      const f32x4_t x = *(const f32x4_t*)(o + (size_t)sc * a.part_rows * p.D);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += fs == 0.f ? 0.f : fs * x[i];
     }
     for (int k = width; k < kWave; k <<= 1)
 #pragma unroll
@@ -437,6 +441,13 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   }
 }
 
+// Waves of an attn_keys workgroup: as many as the LDS of a CU holds tiles for (four
+// tiles of 32 rows a wave, of 64, 128 or 256 elements), at most 8.
+constexpr int attn_keys_waves(int elt_bytes, int head_dim) {
+  const int tiles = 4 * 32 * (head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256) * elt_bytes;
+  return tiles <= (16 << 10) ? 8 : tiles <= (32 << 10) ? 4 : tiles <= (64 << 10) ? 2 : 1;
+}
+
 // Launches of one element type, in files of their own.
 template <typename T> hipError_t launch_attn_rows(const AttnArgs& a, int splits, bool fast, hipStream_t s);
 template <typename T> hipError_t launch_attn_keys(const AttnArgs& a, int splits, bool fast, hipStream_t s);
@@ -447,7 +458,7 @@ template <typename T, int DP> struct RowsShape {
   static constexpr int kKeys = sizeof(T) == 2 && DP <= 128 ? 64 : 32;
 };
 template <typename T, int DP> struct KeysShape {
-  static constexpr int kWaves = sizeof(T) == 4 && DP > 128 ? 1 : 2;
+  static constexpr int kWaves = attn_keys_waves(sizeof(T), DP);
 };
 
 #define SFFN_ATTN_BY_WIDTH(F, T, ...)                  \

@@ -267,7 +267,7 @@ struct AttnTile {
   // value is NaN.  So in tiles with hidden keys such values are looked for, and
   // if there are any, added directly to the outputs of the rows that see them
   // (add_infinite) and replaced by 0 in LDS (clear_infinite).
-  // The 16-byte chunks of the tile are shared by n threads, this being thread i.
+  // The 16-byte chunks of the tile are shared by N threads, this being thread i.
   __device__ static __forceinline__ bool infinite_bits(u32x4_t x) {
     bool bad = false;
 #pragma unroll
@@ -275,13 +275,16 @@ struct AttnTile {
       bad |= (x[j] & 0x7f800000u) == 0x7f800000u || (sizeof(T) == 2 && (x[j] & 0x7f80u) == 0x7f80u);
     return bad;
   }
-  __device__ static __forceinline__ bool find_infinite(const uint8_t* v, int i, int n) {
+  template <int N>
+  __device__ static __forceinline__ bool find_infinite(const uint8_t* v, int i) {
     bool bad = false;
-    for (int at = i * 16; at < kTileBytes; at += n * 16) bad |= infinite_bits(*(const u32x4_t*)(v + at));
+#pragma unroll
+    for (int at = 0; at < kTileBytes; at += N * 16) bad |= infinite_bits(*(const u32x4_t*)(v + at + i * 16));
     return bad;
   }
-  __device__ static __forceinline__ void clear_infinite(uint8_t* v, int i, int n) {
-    for (int at = i * 16; at < kTileBytes; at += n * 16) {
+  template <int N>
+  __device__ static __forceinline__ void clear_infinite(uint8_t* v, int i) {
+    for (int at = i * 16; at < kTileBytes; at += N * 16) {
       u32x4_t x = *(const u32x4_t*)(v + at);
       if (!infinite_bits(x)) continue;
 #pragma unroll

@@ -36,7 +36,7 @@ int64_t key_span(const PagedAttn& p, int64_t tokens) {
 }
 
 // Splits of a key range of at most `span` keys for `groups` workgroups: enough to
-// put `want` workgroups on the GPU, but at least `least` keys each.
+// put `want` workgroups on the GPU, chunks of least .. most keys.
 void split(Plan* pl, const PagedAttn& p, int64_t span, int64_t groups, int64_t want, int least, int most) {
   int64_t n = groups > 0 ? (want + groups - 1) / groups : 1;
   // a range that does not start at a multiple of the chunk touches one more
@@ -67,7 +67,12 @@ Plan plan_keys(int dtype, const PagedAttn& p) {
   pl.tiles_per_seq = (int)(((rows < kKeysMax ? rows : kKeysMax) + kKeysTile - 1) / kKeysTile);
   pl.tiles = p.n_seqs * pl.tiles_per_seq;
   pl.part_rows = (size_t)pl.tiles * p.hkv * kKeysTile;
-  split(&pl, p, key_span(p, kKeysTile / g + 2), (int64_t)pl.tiles * p.hkv, 4 * kCus, 256, 2048);
+  // A wave takes about 1 us for 32 keys (3 us in float32, whose products are 16 times
+  // slower), the join and its launch 5 us: ranges of up to 8 (2) steps a wave
+  // are not split, longer ones into at least half of that.
+  const int steps = attn_keys_waves(dtype == 1 ? 2 : 4, p.D) * 32 * (dtype == 1 ? 8 : 2);
+  const int64_t span = key_span(p, kKeysTile / g + 2);
+  split(&pl, p, span, (int64_t)pl.tiles * p.hkv, 4 * kCus, span <= steps ? steps : steps / 2, steps);
   return pl;
 }
 
