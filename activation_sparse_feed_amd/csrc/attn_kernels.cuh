@@ -128,7 +128,7 @@ __device__ __forceinline__ float finish_lse(float m, float l) {
   return l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
 }
 
-template <typename T, int DP, int KT, int NW, bool FAST>
+template <typename T, int DP, int KT, int NW, int G>
 __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void attn_rows(AttnArgs a) {
   typedef AttnTile<T, DP, KT> Tile;
   constexpr int TM = NW * 32;
@@ -171,8 +171,8 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
   }
   constexpr int kPer = Tile::kLoads / NW;
   static_assert(kPer >= 1, "");
-  TileLoader<T, DP, KT, FAST, kPer, true> load_k;
-  TileLoader<T, DP, KT, FAST, kPer, false> load_v;
+  TileLoader<T, DP, KT, G, kPer, true> load_k;
+  TileLoader<T, DP, KT, G, kPer, false> load_v;
   load_k.init(a, w.seq, hk, b, e, wave * kPer);
   load_v.init(a, w.seq, hk, b, e, wave * kPer);
   const T* q = (const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head;
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
   }
 }
 
-template <typename T, int DP, int NW, bool FAST>
+template <typename T, int DP, int NW, int G>
 __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
   constexpr int KT = 32;
   typedef AttnTile<T, DP, KT> Tile;
@@ -292,8 +292,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
     for (int i = lane * 16; i < Tile::kTileBytes; i += kWave * 16)
       *(u32x4_t*)(k0[wave] + i) = *(u32x4_t*)(k1[wave] + i) = *(u32x4_t*)(v0[wave] + i) =
           *(u32x4_t*)(v1[wave] + i) = u32x4_t{0u, 0u, 0u, 0u};
-  TileLoader<T, DP, KT, FAST, Tile::kLoads, true> load_k;
-  TileLoader<T, DP, KT, FAST, Tile::kLoads, false> load_v;
+  TileLoader<T, DP, KT, G, Tile::kLoads, true> load_k;
+  TileLoader<T, DP, KT, G, Tile::kLoads, false> load_v;
   load_k.init(a, w.seq, hk, b, e, 0);
   load_v.init(a, w.seq, hk, b, e, 0);
   int j0 = (b & ~(KT - 1)) + wave * KT;
@@ -449,18 +449,14 @@ constexpr int attn_keys_waves(int elt_bytes, int head_dim) {
 }
 
 // Launches of one element type, in files of their own.
-template <typename T> hipError_t launch_attn_rows(const AttnArgs& a, int splits, bool fast, hipStream_t s);
-template <typename T> hipError_t launch_attn_keys(const AttnArgs& a, int splits, bool fast, hipStream_t s);
+template <typename T> hipError_t launch_attn_rows(const AttnArgs& a, int splits, int granule, hipStream_t s);
+template <typename T> hipError_t launch_attn_keys(const AttnArgs& a, int splits, int granule, hipStream_t s);
 
-// Key tile and waves of attn_rows, waves of attn_keys.
+// Key tile and waves of attn_rows.
 template <typename T, int DP> struct RowsShape {
   static constexpr int kWaves = 4;
   static constexpr int kKeys = sizeof(T) == 2 && DP <= 128 ? 64 : 32;
 };
-template <typename T, int DP> struct KeysShape {
-  static constexpr int kWaves = attn_keys_waves(sizeof(T), DP);
-};
-
 #define SFFN_ATTN_BY_WIDTH(F, T, ...)                  \
   do {                                                 \
     const int d_ = a.p.D;                              \
@@ -472,26 +468,22 @@ template <typename T, int DP> struct KeysShape {
   } while (0)
 
 template <typename T, int DP>
-hipError_t attn_rows_width(const AttnArgs& a, int splits, bool fast, hipStream_t s) {
-  typedef RowsShape<T, DP> S;
-  const dim3 grid((unsigned)(a.n_tiles * a.p.hkv), (unsigned)splits);
-  if (fast)
-    hipLaunchKernelGGL((attn_rows<T, DP, S::kKeys, S::kWaves, true>), grid, dim3(S::kWaves * 64),
-                       0, s, a);
-  else
-    hipLaunchKernelGGL((attn_rows<T, DP, S::kKeys, S::kWaves, false>), grid, dim3(S::kWaves * 64),
-                       0, s, a);
+hipError_t attn_rows_width(const AttnArgs& a, int splits, int granule, hipStream_t s) {
+  constexpr int kKeys = RowsShape<T, DP>::kKeys, kWaves = RowsShape<T, DP>::kWaves;
+  const dim3 grid((unsigned)(a.n_tiles * a.p.hkv), (unsigned)splits), block(kWaves * 64);
+  if (granule == 16) hipLaunchKernelGGL((attn_rows<T, DP, kKeys, kWaves, 16>), grid, block, 0, s, a);
+  else if (granule == 8) hipLaunchKernelGGL((attn_rows<T, DP, kKeys, kWaves, 8>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((attn_rows<T, DP, kKeys, kWaves, 0>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
 template <typename T, int DP>
-hipError_t attn_keys_width(const AttnArgs& a, int splits, bool fast, hipStream_t s) {
-  typedef KeysShape<T, DP> S;
-  const dim3 grid((unsigned)(a.n_tiles * a.p.hkv), (unsigned)splits);
-  if (fast)
-    hipLaunchKernelGGL((attn_keys<T, DP, S::kWaves, true>), grid, dim3(S::kWaves * 64), 0, s, a);
-  else
-    hipLaunchKernelGGL((attn_keys<T, DP, S::kWaves, false>), grid, dim3(S::kWaves * 64), 0, s, a);
+hipError_t attn_keys_width(const AttnArgs& a, int splits, int granule, hipStream_t s) {
+  constexpr int kWaves = attn_keys_waves(sizeof(T), DP);
+  const dim3 grid((unsigned)(a.n_tiles * a.p.hkv), (unsigned)splits), block(kWaves * 64);
+  if (granule == 16) hipLaunchKernelGGL((attn_keys<T, DP, kWaves, 16>), grid, block, 0, s, a);
+  else if (granule == 8) hipLaunchKernelGGL((attn_keys<T, DP, kWaves, 8>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((attn_keys<T, DP, kWaves, 0>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 

@@ -331,15 +331,18 @@ __device__ __forceinline__ int load_uniform(const int32_t* p) {
 }
 
 // Copies the key rows of one cache (K or V) to LDS, N wave-wide loads per tile and
-// wave.  FAST: the rows of a granule of kG lie in one page (page_size a multiple of
-// 16) and fill their LDS rows (head_dim == kRowElems), so a page is looked up once a
-// granule with scalar instructions and a lane only adds a constant offset; otherwise
-// every lane looks up its own rows.  Pages are looked up one tile ahead.
-template <typename T, int DP, int KT, bool FAST, int N, bool K>
+// wave.  Pages are looked up one tile ahead.
+//   G > 0  page_size is a multiple of G: G neighbouring rows lie in one page, which
+//          is looked up with scalar instructions; a lane adds a constant offset.
+//   G = 0  any page size: lane r looks up row r of the wave's part of a tile, and the
+//          loads get their rows' offsets from it.
+template <typename T, int DP, int KT, int G, int N, bool K>
 struct TileLoader {
   typedef AttnTile<T, DP, KT> Tile;
-  static constexpr int kG = !FAST ? Tile::kRpi : N * Tile::kRpi < 16 ? N * Tile::kRpi : 16;
-  static constexpr int kPerG = kG / Tile::kRpi;  // wave-wide loads of a granule
+  static constexpr int kRows = N * Tile::kRpi;               // of the wave, in a tile
+  static constexpr int kG = G < kRows ? G : kRows;           // rows of one lookup
+  static constexpr int kLookups = G == 0 ? 1 : kRows / (G == 0 ? 1 : kG);
+  static_assert(kRows <= kWave && (G == 0 || kG >= Tile::kRpi), "");
   const int32_t* bt;
   const uint8_t* base;          // of the key head
   uint64_t page_bytes;
@@ -347,7 +350,7 @@ struct TileLoader {
   FastDiv per_page;
   int last_page, first, last;   // keys that exist for this tile: the others repeat one of them
   int i0, n_chunks;             // this wave's first wave-wide load of a tile; chunks of a row
-  int page[N / kPerG], off[N / kPerG];  // of the next tile
+  int page[kLookups], off[kLookups];  // of the next tile
 
   __device__ __forceinline__ void init(const AttnArgs& a, int seq, int hk, int lo, int hi, int load0) {
     const PagedAttn& p = a.p;
@@ -366,34 +369,46 @@ struct TileLoader {
   // The tile of the keys j0 .. j0 + KT - 1 (j0 a multiple of 32).
   __device__ __forceinline__ void look_up(int j0) {
 #pragma unroll
-    for (int n = 0; n < N / kPerG; ++n) {
-      int j = j0 + i0 * Tile::kRpi + n * kG;
-      if constexpr (FAST) j = min(max(j, first & -kG), last & -kG);
-      else j = min(max(j + lane_id() / Tile::kCpr, first), last);
+    for (int n = 0; n < kLookups; ++n) {
+      int j = j0 + i0 * Tile::kRpi;
+      if constexpr (G > 0) j = min(max(j + n * kG, first & -kG), last & -kG);
+      else j = min(max(j + min(lane_id(), kRows - 1), first), last);
       const int pg = per_page.div(j);
       off[n] = j - pg * per_page.d;
-      if constexpr (FAST) page[n] = load_uniform(bt + pg);
+      if constexpr (G > 0) page[n] = load_uniform(bt + pg);
       else page[n] = bt[pg];
     }
   }
 
-  // Starts the loads of the tile that was looked up.
+  // Starts the loads of the tile that was looked up.  Rows that fill their LDS rows
+  // need no mask.
   __device__ __forceinline__ void start(uint8_t* tile) const {
+    if (n_chunks == Tile::kCpr) start_all<false>(tile);
+    else start_all<true>(tile);
+  }
+  template <bool MASK>
+  __device__ __forceinline__ void start_all(uint8_t* tile) const {
     const int rin = lane_id() / Tile::kCpr, chunk = lane_id() % Tile::kCpr;
+    const uint64_t lane_row = (uint32_t)min(max(page[0], 0), last_page) * page_bytes + off[0] * token_bytes;
 #pragma unroll
-    for (int g = 0; g < N / kPerG; ++g) {
-      const uint32_t pg = (uint32_t)min(max(page[g], 0), last_page);
-      const uint8_t* row = base + (pg * page_bytes + off[g] * token_bytes);
-#pragma unroll
-      for (int m = 0; m < kPerG; ++m) {
-        const int i = i0 + g * kPerG + m, r = i * Tile::kRpi + rin;
-        const int c = chunk ^ (K ? Tile::swz_k(r) : Tile::swz_v(r));
-        uint8_t* to = tile + i * 1024;
-        if constexpr (FAST)
-          copy16(row + m * Tile::kRpi * token_bytes + ((uint32_t)rin * (uint32_t)token_bytes + c * 16), to);
-        else if (c < n_chunks)
-          copy16(row + c * 16, to);
+    for (int n = 0; n < N; ++n) {
+      const int r = (i0 + n) * Tile::kRpi + rin;  // row of the tile
+      const int c = chunk ^ (K ? Tile::swz_k(r) : Tile::swz_v(r));
+      uint8_t* to = tile + (i0 + n) * 1024;
+      const uint8_t* row;
+      uint32_t lane_bytes = c * 16;
+      if constexpr (G > 0) {
+        const int at = n * Tile::kRpi, g = at / kG;
+        row = base + ((uint32_t)min(max(page[g], 0), last_page) * page_bytes +
+                      (off[g] + at % kG) * token_bytes);
+        lane_bytes += (uint32_t)rin * (uint32_t)token_bytes;
+      } else {
+        const int from = n * Tile::kRpi + rin;
+        const uint32_t lo = __shfl((uint32_t)lane_row, from, kWave);
+        const uint32_t hi = __shfl((uint32_t)(lane_row >> 32), from, kWave);
+        row = base + (((uint64_t)hi << 32) | lo);
       }
+      if (!MASK || c < n_chunks) copy16(row + lane_bytes, to);
     }
   }
 };

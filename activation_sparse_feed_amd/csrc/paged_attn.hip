@@ -6,10 +6,10 @@
 
 namespace sffn {
 
-template <> hipError_t launch_attn_rows<uint16_t>(const AttnArgs&, int, bool, hipStream_t);
-template <> hipError_t launch_attn_rows<float>(const AttnArgs&, int, bool, hipStream_t);
-template <> hipError_t launch_attn_keys<uint16_t>(const AttnArgs&, int, bool, hipStream_t);
-template <> hipError_t launch_attn_keys<float>(const AttnArgs&, int, bool, hipStream_t);
+template <> hipError_t launch_attn_rows<uint16_t>(const AttnArgs&, int, int, hipStream_t);
+template <> hipError_t launch_attn_rows<float>(const AttnArgs&, int, int, hipStream_t);
+template <> hipError_t launch_attn_keys<uint16_t>(const AttnArgs&, int, int, hipStream_t);
+template <> hipError_t launch_attn_keys<float>(const AttnArgs&, int, int, hipStream_t);
 
 namespace {
 
@@ -107,14 +107,14 @@ void place(AttnArgs* a, const Plan& pl, void* ws) {
 template <typename T>
 hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipStream_t s) {
   const PagedAttn& p = a.p;
-  // see TileLoader: granules of 16 rows in one page, full LDS rows, and lane
-  // offsets of less than 32 rows in 32 bits
-  const bool fast = (p.D == 64 || p.D == 128 || p.D == 256) && p.page_size % 16 == 0 &&
-                    p.kc_token < (1 << 24) && p.vc_token < (1 << 24);
+  // see TileLoader: rows looked up together, lane offsets of less than 32 rows in
+  // 32 bits
+  const bool near = p.kc_token < (1 << 24) && p.vc_token < (1 << 24);
+  const int granule = !near ? 0 : p.page_size % 16 == 0 ? 16 : p.page_size % 8 == 0 ? 8 : 0;
   hipError_t e = hipSuccess;
   if (rows.used) {
     place(&a, rows, (char*)ws + keys.bytes);
-    e = launch_attn_rows<T>(a, rows.splits, fast, s);
+    e = launch_attn_rows<T>(a, rows.splits, granule, s);
     if (e != hipSuccess) return e;
     if (rows.splits > 1) {
       hipLaunchKernelGGL((attn_join<T, kRowsTile>), dim3((unsigned)(rows.tiles * p.hkv), 8),
@@ -125,7 +125,7 @@ hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipS
   }
   if (keys.used) {
     place(&a, keys, ws);
-    e = launch_attn_keys<T>(a, keys.splits, fast, s);
+    e = launch_attn_keys<T>(a, keys.splits, granule, s);
     if (e != hipSuccess) return e;
     if (keys.splits > 1) {
       const int64_t most = (int64_t)p.max_q * a.g < kKeysTile ? (int64_t)p.max_q * a.g : kKeysTile;
