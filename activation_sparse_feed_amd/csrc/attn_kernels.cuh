@@ -75,18 +75,6 @@ __device__ __forceinline__ Work find_tile(const AttnArgs& a, int t) {
   return w;
 }
 
-// attn_keys' tile number t: every sequence has tiles_per_seq of them, taken where
-// it has so many rows, and at most max_rows.
-__device__ __forceinline__ Work sequence_tile(const AttnArgs& a, int t) {
-  Work w;
-  const int s = t / a.tiles_per_seq;
-  read_sequence(a.p, s, &w);
-  const int rows = w.nq * a.g;
-  w.tile = t - s * a.tiles_per_seq;
-  if (w.tile * 32 >= rows || rows > a.max_rows) w.tile = -1;
-  return w;
-}
-
 // The keys [lo, hi) that token i (0 .. nq - 1) sees; lo == hi: none.
 __device__ __forceinline__ void key_range(const PagedAttn& p, const Work& w, int i, int* lo, int* hi) {
   const int pos = w.nkv - w.nq + i;
@@ -102,11 +90,101 @@ __device__ __forceinline__ int split_range(const AttnArgs& a, int split, int lo,
     *b = *e = lo;
     return 1;
   }
-  const int c0 = lo / a.chunk, n = (hi - 1) / a.chunk - c0 + 1;
-  *b = max(lo, (c0 + split) * a.chunk);
-  *e = min((int64_t)hi, (int64_t)(c0 + split + 1) * a.chunk);
+  const int c0 = a.chunk.div(lo), n = a.chunk.div(hi - 1) - c0 + 1;
+  *b = max(lo, (c0 + split) * a.chunk.d);
+  *e = (int)min((int64_t)hi, (int64_t)(c0 + split + 1) * a.chunk.d);
   return n;
 }
+
+// Inclusive prefix sum over the wave: shifts by 1, 2, 4, 8 within rows of 16 lanes,
+// then the last lane of a row to the next row(s).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int prefix_sum(int v) {
+  v = dpp_add<0x111, 0xf>(v);
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
+  return dpp_add<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+}
+
+// Row tiles of 32 of the sequences that attn_keys takes (1 .. max_rows rows), and the
+// splits of their key ranges: one range for all tiles of a sequence.
+struct KeysWork {
+  Work w;
+  int split, n_split, lo, hi;  // of the sequence; split: number within n_split
+};
+
+__device__ __forceinline__ void sequence_range(const AttnArgs& a, KeysWork* k) {
+  int x, y;
+  key_range(a.p, k->w, 0, &k->lo, &y);
+  key_range(a.p, k->w, max(k->w.nq - 1, 0), &x, &k->hi);
+  k->n_split = split_range(a, 0, k->lo, k->hi, &x, &y);
+}
+
+// The items (sequence, tile, split) of attn_keys, numbered through; 64 sequences are
+// held by the lanes of a wave at a time, and the numbers asked for only grow.
+struct KeysItems {
+  int s0, base, total;          // first sequence of the 64, items before and in them
+  int before, n;                // lane's items before its sequence, and of it
+  KeysWork k;                   // lane's sequence
+
+  __device__ __forceinline__ void group(const AttnArgs& a, int first) {
+    const PagedAttn& p = a.p;
+    s0 = first;
+    const int s = s0 + lane_id();
+    n = 0;
+    k.w.seq = s;
+    k.w.q0 = k.w.nq = k.w.nkv = 0;
+    if (s < p.n_seqs) {
+      const int b = min(max(p.q_start[s], 0), p.T), e = min(max(p.q_start[s + 1], b), p.T);
+      k.w.q0 = b;
+      k.w.nq = e - b;
+      k.w.nkv = min(max(p.kv_len[s], 0), p.max_kv);
+    }
+    const int rows = k.w.nq * a.g;
+    sequence_range(a, &k);
+    if (rows > 0 && rows <= a.max_rows) n = (rows + 31) / 32 * k.n_split;
+    before = prefix_sum(n);
+    total = __builtin_amdgcn_readlane(before, kWave - 1);
+    before -= n;
+  }
+  __device__ __forceinline__ void init(const AttnArgs& a) {
+    base = 0;
+    group(a, 0);
+  }
+  // Item v, or false past the last one.
+  __device__ __forceinline__ bool get(const AttnArgs& a, int v, KeysWork* out) {
+    while (v - base >= total) {
+      base += total;
+      if (s0 + kWave >= a.p.n_seqs) {
+        total = 0;
+        s0 = a.p.n_seqs;
+        return false;
+      }
+      group(a, s0 + kWave);
+    }
+    const int u = v - base;
+    const int lane = (int)__builtin_ctzll(__ballot(u >= before && u < before + n));
+    out->w.seq = s0 + lane;
+    out->w.q0 = __builtin_amdgcn_readlane(k.w.q0, lane);
+    out->w.nq = __builtin_amdgcn_readlane(k.w.nq, lane);
+    out->w.nkv = __builtin_amdgcn_readlane(k.w.nkv, lane);
+    out->lo = __builtin_amdgcn_readlane(k.lo, lane);
+    out->hi = __builtin_amdgcn_readlane(k.hi, lane);
+    out->n_split = __builtin_amdgcn_readlane(k.n_split, lane);
+    out->split = u - __builtin_amdgcn_readlane(before, lane);
+    out->w.tile = 0;
+    while (out->split >= out->n_split) {  // few tiles
+      out->split -= out->n_split;
+      ++out->w.tile;
+    }
+    return true;
+  }
+};
 
 // Writes one row's outputs (lane: d = 8 * quad + 4 * half + 0..3 of each 32): the
 // result, or its part of a split.
@@ -264,7 +342,7 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
   }
 }
 
-template <typename T, int DP, int NW, int G>
+template <typename T, int DP, int NW, int G, bool COMPACT>
 __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
   constexpr int KT = 32;
   typedef AttnTile<T, DP, KT> Tile;
@@ -272,115 +350,142 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
       v0[NW][Tile::kTileBytes], v1[NW][Tile::kTileBytes];
   __shared__ float ml[NW][32][2];
   const PagedAttn& p = a.p;
-  const int hk = (int)blockIdx.x % p.hkv, split = blockIdx.y, t = (int)blockIdx.x / p.hkv;
-  const Work w = sequence_tile(a, t);
-  if (w.tile < 0) return;
-  const int r0 = w.tile * 32, rows = min(32, w.nq * a.g - r0);
   const int wave = uniform((int)threadIdx.x / kWave), lane = lane_id(), half = lane >> 5;
-  int lo, hi, b, e, x, y;
-  key_range(p, w, a.group.div(r0), &lo, &y);
-  key_range(p, w, a.group.div(r0 + rows - 1), &x, &hi);
-  const int n_split = split_range(a, split, lo, hi, &b, &e);
-  if (split >= n_split) return;
-  const int r = r0 + min(lane & 31, rows - 1);
-  const int token = a.group.div(r), head = hk * a.g + r - token * a.g;
-  int row_lo, row_hi;
-  key_range(p, w, token, &row_lo, &row_hi);
-  Tile tile;
-  tile.init();
   if (p.D != DP)  // chunks that are read, but that no load writes
     for (int i = lane * 16; i < Tile::kTileBytes; i += kWave * 16)
       *(u32x4_t*)(k0[wave] + i) = *(u32x4_t*)(k1[wave] + i) = *(u32x4_t*)(v0[wave] + i) =
           *(u32x4_t*)(v1[wave] + i) = u32x4_t{0u, 0u, 0u, 0u};
-  TileLoader<T, DP, KT, G, Tile::kLoads, true> load_k;
-  TileLoader<T, DP, KT, G, Tile::kLoads, false> load_v;
-  load_k.init(a, w.seq, hk, b, e, 0);
-  load_v.init(a, w.seq, hk, b, e, 0);
-  int j0 = (b & ~(KT - 1)) + wave * KT;
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // the zeros are written (lgkmcnt)
-  auto load = [&](int j, uint8_t* k, uint8_t* v) __attribute__((always_inline)) {
-    load_k.start(k);
-    load_v.start(v);
-    load_k.look_up(j + NW * KT);
-    load_v.look_up(j + NW * KT);
-  };
-  if (j0 < e) {
-    load_k.look_up(j0);
-    load_v.look_up(j0);
-    load(j0, k0[wave], v0[wave]);
-    tile.load_q((const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D, a.negate != 0);
-  }
-  auto iteration = [&](uint8_t* k, uint8_t* v, uint8_t* k_next, uint8_t* v_next) __attribute__((always_inline)) {
-    wait_loads<0>();
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    if (j0 + NW * KT < e) load(j0 + NW * KT, k_next, v_next);
-    const bool whole = j0 >= x && j0 + KT <= y;
-    if (!whole && __any(Tile::template find_infinite<kWave>(v, lane))) {
-      tile.add_infinite(v, j0, row_lo, row_hi);
-      Tile::template clear_infinite<kWave>(v, lane);
-    }
-    f32x16_t s = tile.scores(k);
-    if (!whole) Tile::hide(s, j0, row_lo, row_hi);
-    tile.raise(s, a.c);
-    tile.weights(s, a.c);
-    tile.accumulate(v, s);
-    j0 += NW * KT;
-  };
-  while (j0 < e) {
-    iteration(k0[wave], v0[wave], k1[wave], v1[wave]);
-    if (j0 >= e) break;
-    iteration(k1[wave], v1[wave], k0[wave], v0[wave]);
-  }
-  tile.l = sum_halves(tile.l);
-  // Join the waves: each leaves its rows in its K arrays, 32 x 32 floats for each
-  // block of 32 outputs, row r's 16-byte chunk c at c ^ (r % 8).
-  constexpr int kPerArray = Tile::kTileBytes / 4096;
-  static_assert(kPerArray * 2 >= Tile::kDt, "");
-  auto part = [&](int wv, int d) { return (d < kPerArray ? k0[wv] + d * 4096 : k1[wv] + (d - kPerArray) * 4096); };
-  {
-    const int row = lane & 31;
-#pragma unroll
-    for (int d = 0; d < Tile::kDt; ++d)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        store4<float>((float*)(part(wave, d) + row * 128 + (((2 * i + half) ^ (row & 7)) << 4)),
-                      tile.o[d][4 * i], tile.o[d][4 * i + 1], tile.o[d][4 * i + 2], tile.o[d][4 * i + 3]);
-    if (half == 0) {
-      ml[wave][row][0] = tile.m * a.c;
-      ml[wave][row][1] = tile.l;
-    }
-  }
-  __syncthreads();
-  const int quads = p.D / 4;
-  for (int i = threadIdx.x; i < rows * quads; i += NW * 64) {
-    const int rr = i / quads, d = (i - rr * quads) * 4;
-    float m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int k = 0; k < NW; ++k) m = fmaxf(m, ml[k][rr][0]);
-    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < NW; ++k) {
-      const float mk = ml[k][rr][0];
-      const float f = mk == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mk - m);
-      l += f * ml[k][rr][1];
-      if (mk != -INFINITY)
-        v += f * *(const f32x4_t*)(part(k, d / 32) + rr * 128 + (((d % 32 / 4) ^ (rr & 7)) << 4));
-    }
-    const int tk = a.group.div(r0 + rr), hd = hk * a.g + r0 + rr - tk * a.g;
-    if (n_split == 1) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      store4<T>((T*)p.out + (int64_t)(w.q0 + tk) * p.o_token + hd * p.o_head + d, v[0] * inv,
-                v[1] * inv, v[2] * inv, v[3] * inv);
-      if (d == 0 && p.lse != nullptr) p.lse[(int64_t)(w.q0 + tk) * p.hq + hd] = finish_lse(m, l);
+  // Items (sequence, tile, split) are numbered from bounds of the lengths: the item of
+  // a workgroup is at hand, but may not exist.  A workgroup without work still waits
+  // for its place in LDS, so where most are expected to be of that kind (COMPACT:
+  // chunks of prompts beside single tokens) only the items that exist are numbered,
+  // for 1.5 us to look over the sequences, and a limited grid goes over them.
+  KeysItems items;
+  if constexpr (COMPACT) items.init(a);
+  for (int item = blockIdx.x;; item += gridDim.x) {
+    KeysWork kw;
+    const int hk = item % p.hkv;
+    if constexpr (COMPACT) {
+      if (!items.get(a, item / p.hkv, &kw)) break;
     } else {
-      const size_t slot = split * a.part_rows + (size_t)blockIdx.x * 32 + rr;
-      *(f32x4_t*)(a.part_o + slot * p.D + d) = v;
-      if (d == 0) {
-        a.part_ml[2 * slot] = m;
-        a.part_ml[2 * slot + 1] = l;
+      kw.split = blockIdx.y;
+      const int t = item / p.hkv, s = t / a.tiles_per_seq;
+      read_sequence(p, s, &kw.w);
+      kw.w.tile = t - s * a.tiles_per_seq;
+      const int all = kw.w.nq * a.g;
+      if (kw.w.tile * 32 >= all || all > a.max_rows) break;
+      sequence_range(a, &kw);
+      if (kw.split >= kw.n_split) break;
+    }
+    const Work w = kw.w;
+    const int r0 = w.tile * 32, rows = min(32, w.nq * a.g - r0);
+    // the tile's keys in this split
+    int lo, hi, b, e, x, y;
+    key_range(p, w, a.group.div(r0), &lo, &y);
+    key_range(p, w, a.group.div(r0 + rows - 1), &x, &hi);
+    split_range(a, kw.split, kw.lo, kw.hi, &b, &e);
+    b = max(b, lo);
+    e = min(e, hi);
+    const int r = r0 + min(lane & 31, rows - 1);
+    const int token = a.group.div(r), head = hk * a.g + r - token * a.g;
+    int row_lo, row_hi;
+    key_range(p, w, token, &row_lo, &row_hi);
+    Tile tile;
+    tile.init();
+    TileLoader<T, DP, KT, G, Tile::kLoads, true> load_k;
+    TileLoader<T, DP, KT, G, Tile::kLoads, false> load_v;
+    load_k.init(a, w.seq, hk, b, e, 0);
+    load_v.init(a, w.seq, hk, b, e, 0);
+    int j0 = (b & ~(KT - 1)) + wave * KT;
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // the zeros are written (lgkmcnt)
+    auto load = [&](int j, uint8_t* k, uint8_t* v) __attribute__((always_inline)) {
+      load_k.start(k);
+      load_v.start(v);
+      load_k.look_up(j + NW * KT);
+      load_v.look_up(j + NW * KT);
+    };
+    if (b < e && j0 < e) {
+      load_k.look_up(j0);
+      load_v.look_up(j0);
+      load(j0, k0[wave], v0[wave]);
+      tile.load_q((const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D, a.negate != 0);
+    }
+    auto iteration = [&](uint8_t* k, uint8_t* v, uint8_t* k_next, uint8_t* v_next) __attribute__((always_inline)) {
+      wait_loads<0>();
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      if (j0 + NW * KT < e) load(j0 + NW * KT, k_next, v_next);
+      const bool whole = j0 >= x && j0 + KT <= y;
+      if (!whole && __any(Tile::template find_infinite<kWave>(v, lane))) {
+        tile.add_infinite(v, j0, row_lo, row_hi);
+        Tile::template clear_infinite<kWave>(v, lane);
+      }
+      f32x16_t s = tile.scores(k);
+      if (!whole) Tile::hide(s, j0, row_lo, row_hi);
+      tile.raise(s, a.c);
+      tile.weights(s, a.c);
+      tile.accumulate(v, s);
+      j0 += NW * KT;
+    };
+    while (b < e && j0 < e) {
+      iteration(k0[wave], v0[wave], k1[wave], v1[wave]);
+      if (j0 >= e) break;
+      iteration(k1[wave], v1[wave], k0[wave], v0[wave]);
+    }
+    tile.l = sum_halves(tile.l);
+    // Join the waves: each leaves its rows in its V arrays (K's must keep the zeros of
+    // chunks beyond head_dim), 32 x 32 floats for each block of 32 outputs, row r's
+    // 16-byte chunk c at c ^ (r % 8).
+    constexpr int kPerArray = Tile::kTileBytes / 4096;
+    static_assert(kPerArray * 2 >= Tile::kDt, "");
+    auto part = [&](int wv, int d) { return (d < kPerArray ? v0[wv] + d * 4096 : v1[wv] + (d - kPerArray) * 4096); };
+    {
+      const int row = lane & 31;
+#pragma unroll
+      for (int d = 0; d < Tile::kDt; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          store4<float>((float*)(part(wave, d) + row * 128 + (((2 * i + half) ^ (row & 7)) << 4)),
+                        tile.o[d][4 * i], tile.o[d][4 * i + 1], tile.o[d][4 * i + 2], tile.o[d][4 * i + 3]);
+      if (half == 0) {
+        ml[wave][row][0] = tile.m * a.c;
+        ml[wave][row][1] = tile.l;
       }
     }
+    __syncthreads();
+    const int quads = p.D / 4;
+    for (int i = threadIdx.x; i < rows * quads; i += NW * 64) {
+      const int rr = i / quads, d = (i - rr * quads) * 4;
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) m = fmaxf(m, ml[k][rr][0]);
+      f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < NW; ++k) {
+        const float mk = ml[k][rr][0];
+        const float f = mk == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mk - m);
+        l += f * ml[k][rr][1];
+        if (mk != -INFINITY)
+          v += f * *(const f32x4_t*)(part(k, d / 32) + rr * 128 + (((d % 32 / 4) ^ (rr & 7)) << 4));
+      }
+      const int tk = a.group.div(r0 + rr), hd = hk * a.g + r0 + rr - tk * a.g;
+      if (kw.n_split == 1) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        store4<T>((T*)p.out + (int64_t)(w.q0 + tk) * p.o_token + hd * p.o_head + d, v[0] * inv,
+                  v[1] * inv, v[2] * inv, v[3] * inv);
+        if (d == 0 && p.lse != nullptr) p.lse[(int64_t)(w.q0 + tk) * p.hq + hd] = finish_lse(m, l);
+      } else {
+        const size_t slot = kw.split * a.part_rows +
+                            ((size_t)(w.seq * a.tiles_per_seq + w.tile) * p.hkv + hk) * 32 + rr;
+        *(f32x4_t*)(a.part_o + slot * p.D + d) = v;
+        if (d == 0) {
+          a.part_ml[2 * slot] = m;
+          a.part_ml[2 * slot + 1] = l;
+        }
+      }
+    }
+    if constexpr (!COMPACT) break;
+    __syncthreads();  // the waves' results are read before the next item's tiles arrive
   }
 }
 
@@ -391,13 +496,29 @@ template <typename T, int TM>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   const PagedAttn& p = a.p;
   const int hk = (int)blockIdx.x % p.hkv, t = (int)blockIdx.x / p.hkv;
-  const Work w = TM == 32 ? sequence_tile(a, t) : find_tile<TM>(a, t);
-  if (w.tile < 0) return;
+  Work w;
+  int n;
+  if constexpr (TM == 32) {
+    KeysWork k;
+    const int s = t / a.tiles_per_seq;
+    read_sequence(p, s, &k.w);
+    const int all = k.w.nq * a.g;
+    k.w.tile = t - s * a.tiles_per_seq;
+    if (k.w.tile * 32 >= all || all > a.max_rows) return;
+    sequence_range(a, &k);
+    n = k.n_split;
+    w = k.w;
+  } else {
+    w = find_tile<TM>(a, t);
+    if (w.tile < 0) return;
+  }
   const int rows = w.nq * a.g, r0 = w.tile * TM, r1 = min(r0 + TM, rows) - 1;
-  int lo, hi, b, e, x, y;
-  key_range(p, w, a.group.div(r0), &lo, &y);
-  key_range(p, w, a.group.div(r1), &x, &hi);
-  const int n = split_range(a, 0, lo, hi, &b, &e);
+  if constexpr (TM != 32) {
+    int lo, hi, b, e, x, y;
+    key_range(p, w, a.group.div(r0), &lo, &y);
+    key_range(p, w, a.group.div(r1), &x, &hi);
+    n = split_range(a, 0, lo, hi, &b, &e);
+  }
   if (n == 1) return;  // written by the kernel before
   const int lane = lane_id();
   int width = 1;  // lanes of one split's outputs
@@ -441,6 +562,8 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   }
 }
 
+constexpr int kCus = 256;
+
 // Waves of an attn_keys workgroup: as many as the LDS of a CU holds tiles for (four
 // tiles of 32 rows a wave, of 64, 128 or 256 elements), at most 8.
 constexpr int attn_keys_waves(int elt_bytes, int head_dim) {
@@ -449,8 +572,8 @@ constexpr int attn_keys_waves(int elt_bytes, int head_dim) {
 }
 
 // Launches of one element type, in files of their own.
-template <typename T> hipError_t launch_attn_rows(const AttnArgs& a, int splits, int granule, hipStream_t s);
-template <typename T> hipError_t launch_attn_keys(const AttnArgs& a, int splits, int granule, hipStream_t s);
+template <typename T> hipError_t launch_attn_rows(const AttnArgs& a, int granule, hipStream_t s);
+template <typename T> hipError_t launch_attn_keys(const AttnArgs& a, int granule, bool compact, hipStream_t s);
 
 // Key tile and waves of attn_rows.
 template <typename T, int DP> struct RowsShape {
@@ -468,9 +591,9 @@ template <typename T, int DP> struct RowsShape {
   } while (0)
 
 template <typename T, int DP>
-hipError_t attn_rows_width(const AttnArgs& a, int splits, int granule, hipStream_t s) {
+hipError_t attn_rows_width(const AttnArgs& a, int granule, hipStream_t s) {
   constexpr int kKeys = RowsShape<T, DP>::kKeys, kWaves = RowsShape<T, DP>::kWaves;
-  const dim3 grid((unsigned)(a.n_tiles * a.p.hkv), (unsigned)splits), block(kWaves * 64);
+  const dim3 grid((unsigned)(a.n_tiles * a.p.hkv), (unsigned)a.splits), block(kWaves * 64);
   if (granule == 16) hipLaunchKernelGGL((attn_rows<T, DP, kKeys, kWaves, 16>), grid, block, 0, s, a);
   else if (granule == 8) hipLaunchKernelGGL((attn_rows<T, DP, kKeys, kWaves, 8>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((attn_rows<T, DP, kKeys, kWaves, 0>), grid, block, 0, s, a);
@@ -478,12 +601,18 @@ hipError_t attn_rows_width(const AttnArgs& a, int splits, int granule, hipStream
 }
 
 template <typename T, int DP>
-hipError_t attn_keys_width(const AttnArgs& a, int splits, int granule, hipStream_t s) {
+hipError_t attn_keys_width(const AttnArgs& a, int granule, bool compact, hipStream_t s) {
   constexpr int kWaves = attn_keys_waves(sizeof(T), DP);
-  const dim3 grid((unsigned)(a.n_tiles * a.p.hkv), (unsigned)splits), block(kWaves * 64);
-  if (granule == 16) hipLaunchKernelGGL((attn_keys<T, DP, kWaves, 16>), grid, block, 0, s, a);
-  else if (granule == 8) hipLaunchKernelGGL((attn_keys<T, DP, kWaves, 8>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((attn_keys<T, DP, kWaves, 0>), grid, block, 0, s, a);
+  const int64_t items = (int64_t)a.n_tiles * a.p.hkv * a.splits, most = 8 * kCus;
+  const dim3 all((unsigned)(a.n_tiles * a.p.hkv), (unsigned)a.splits);
+  const dim3 some((unsigned)(items < most ? items : most)), block(kWaves * 64);
+#define SFFN_KEYS(G)                                                                            \
+  if (compact) hipLaunchKernelGGL((attn_keys<T, DP, kWaves, G, true>), some, block, 0, s, a);   \
+  else hipLaunchKernelGGL((attn_keys<T, DP, kWaves, G, false>), all, block, 0, s, a)
+  if (granule == 16) { SFFN_KEYS(16); }
+  else if (granule == 8) { SFFN_KEYS(8); }
+  else { SFFN_KEYS(0); }
+#undef SFFN_KEYS
   return hipGetLastError();
 }
 

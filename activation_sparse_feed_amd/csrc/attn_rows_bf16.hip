@@ -4,8 +4,8 @@
 namespace sffn {
 
 template <>
-hipError_t launch_attn_rows<uint16_t>(const AttnArgs& a, int splits, int granule, hipStream_t s) {
-  SFFN_ATTN_BY_WIDTH(attn_rows_width, uint16_t, a, splits, granule, s);
+hipError_t launch_attn_rows<uint16_t>(const AttnArgs& a, int granule, hipStream_t s) {
+  SFFN_ATTN_BY_WIDTH(attn_rows_width, uint16_t, a, granule, s);
 }
 
 }  // namespace sffn

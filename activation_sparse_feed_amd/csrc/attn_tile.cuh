@@ -55,10 +55,11 @@ struct AttnArgs {
   int g;                 // query heads per key head
   float c;               // |scale| log2(e): scores are kept as q . k, exponents in base 2
   int negate;            // scale < 0: q is negated
-  int chunk;             // keys per split, a multiple of the key tile
+  FastDiv chunk;         // keys per split, a multiple of the key tile
   int min_rows;          // attn_rows takes sequences with more rows than this
   int max_rows;          // attn_keys takes sequences with at most so many
   int tiles_per_seq;     // attn_keys
+  int splits;            // (bound of) splits of a key range
   int n_tiles;           // (bound of) row tiles of one key head
   float* part_o;         // [split][slot][D] outputs before the division, for split rows
   float* part_ml;        // [split][slot][2] maximum (base 2) and sum

@@ -6,17 +6,16 @@
 
 namespace sffn {
 
-template <> hipError_t launch_attn_rows<uint16_t>(const AttnArgs&, int, int, hipStream_t);
-template <> hipError_t launch_attn_rows<float>(const AttnArgs&, int, int, hipStream_t);
-template <> hipError_t launch_attn_keys<uint16_t>(const AttnArgs&, int, int, hipStream_t);
-template <> hipError_t launch_attn_keys<float>(const AttnArgs&, int, int, hipStream_t);
+template <> hipError_t launch_attn_rows<uint16_t>(const AttnArgs&, int, hipStream_t);
+template <> hipError_t launch_attn_rows<float>(const AttnArgs&, int, hipStream_t);
+template <> hipError_t launch_attn_keys<uint16_t>(const AttnArgs&, int, bool, hipStream_t);
+template <> hipError_t launch_attn_keys<float>(const AttnArgs&, int, bool, hipStream_t);
 
 namespace {
 
 constexpr int kRowsTile = 128;  // rows of an attn_rows workgroup
 constexpr int kKeysTile = 32;   // rows of an attn_keys workgroup
 constexpr int kKeysMax = 64;    // rows of a sequence that attn_keys takes
-constexpr int kCus = 256;
 constexpr int kMaxSplits = 64;  // lanes of the join
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -71,7 +70,7 @@ Plan plan_keys(int dtype, const PagedAttn& p) {
   // slower), the join and its launch 5 us: ranges of up to 8 (2) steps a wave
   // are not split, longer ones into at least half of that.
   const int steps = attn_keys_waves(dtype == 1 ? 2 : 4, p.D) * 32 * (dtype == 1 ? 8 : 2);
-  const int64_t span = key_span(p, kKeysTile / g + 2);
+  const int64_t span = key_span(p, kKeysMax / g + 1);
   split(&pl, p, span, (int64_t)pl.tiles * p.hkv, 4 * kCus, span <= steps ? steps : steps / 2, steps);
   return pl;
 }
@@ -94,10 +93,11 @@ Plan plan_rows(int dtype, const PagedAttn& p, bool with_keys) {
 }
 
 void place(AttnArgs* a, const Plan& pl, void* ws) {
-  a->chunk = pl.chunk;
+  a->chunk = FastDiv::make(pl.chunk);
   a->min_rows = pl.min_rows;
   a->max_rows = pl.max_rows;
   a->tiles_per_seq = pl.tiles_per_seq;
+  a->splits = pl.splits;
   a->n_tiles = pl.tiles;
   a->part_rows = pl.part_rows;
   a->part_o = (float*)ws;
@@ -114,10 +114,10 @@ hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipS
   hipError_t e = hipSuccess;
   if (rows.used) {
     place(&a, rows, (char*)ws + keys.bytes);
-    e = launch_attn_rows<T>(a, rows.splits, granule, s);
+    e = launch_attn_rows<T>(a, granule, s);
     if (e != hipSuccess) return e;
     if (rows.splits > 1) {
-      hipLaunchKernelGGL((attn_join<T, kRowsTile>), dim3((unsigned)(rows.tiles * p.hkv), 8),
+      hipLaunchKernelGGL((attn_join<T, kRowsTile>), dim3((unsigned)(rows.tiles * p.hkv), 32),
                          dim3(256), 0, s, a);
       e = hipGetLastError();
       if (e != hipSuccess) return e;
@@ -125,7 +125,8 @@ hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipS
   }
   if (keys.used) {
     place(&a, keys, ws);
-    e = launch_attn_keys<T>(a, keys.splits, granule, s);
+
+    e = launch_attn_keys<T>(a, granule, rows.used, s);
     if (e != hipSuccess) return e;
     if (keys.splits > 1) {
       const int64_t most = (int64_t)p.max_q * a.g < kKeysTile ? (int64_t)p.max_q * a.g : kKeysTile;
