@@ -489,11 +489,14 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
   }
 }
 
-// Joins the splits of the rows of one tile (TM rows; 32: of attn_keys), a wave for
-// each row: its lanes hold the maxima and sums of up to 64 splits, then D / 4 lanes
-// a split's outputs, several splits side by side.
+// Joins the splits of the rows of one tile (TM rows; 32: of attn_keys).  A wave's lanes
+// hold the maxima and sums of up to 64 splits, then D / 4 lanes a split's outputs,
+// several splits side by side.  attn_keys' rows are few and may have many splits:
+// the four waves of a workgroup share a row; otherwise each has its own.
 template <typename T, int TM>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
+  constexpr int kShare = TM == 32 ? 4 : 1;  // waves of a row
+  __shared__ f32x4_t sums[kShare][kWave];
   const PagedAttn& p = a.p;
   const int hk = (int)blockIdx.x % p.hkv, t = (int)blockIdx.x / p.hkv;
   Work w;
@@ -520,11 +523,12 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
     n = split_range(a, 0, lo, hi, &b, &e);
   }
   if (n == 1) return;  // written by the kernel before
-  const int lane = lane_id();
+  const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
   int width = 1;  // lanes of one split's outputs
   while (width * 4 < p.D) width *= 2;
   const int side = kWave / width, sub = lane / width, d = (lane & (width - 1)) * 4;
-  for (int r = r0 + (int)blockIdx.y * 4 + (int)threadIdx.x / kWave; r <= r1; r += (int)gridDim.y * 4) {
+  const int first = r0 + (kShare == 4 ? (int)blockIdx.y : (int)blockIdx.y * 4 + wave);
+  for (int r = first; r <= r1; r += (int)gridDim.y * (4 / kShare)) {
     const size_t slot = ((size_t)t * p.hkv + hk) * TM + (r - r0);
     float ms = -INFINITY, ls = 0.f;
     if (lane < n) {
@@ -542,7 +546,7 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
     // loads without conditions, so that they are in flight together: a split past the
     // last one repeats it with a factor of 0
 #pragma unroll 8
-    for (int s0 = 0; s0 < n; s0 += side) {
+    for (int s0 = kShare == 4 ? wave * side : 0; s0 < n; s0 += side * kShare) {
       const int s = s0 + sub, sc = min(s, n - 1);
       const float fc = __shfl(f, sc, kWave), fs = s < n ? fc : 0.f;
       const f32x4_t x = *(const f32x4_t*)(o + (size_t)sc * a.part_rows * p.D);
@@ -552,13 +556,22 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
     for (int k = width; k < kWave; k <<= 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], k, kWave);
+    if constexpr (kShare == 4) {
+      sums[wave][lane] = v;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kShare; ++k) v = k == 0 ? sums[0][lane] : v + sums[k][lane];
+    }
     const int token = a.group.div(r), head = hk * a.g + r - token * a.g;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (sub == 0 && d < p.D)
-      store4<T>((T*)p.out + (int64_t)(w.q0 + token) * p.o_token + head * p.o_head + d, v[0] * inv,
-                v[1] * inv, v[2] * inv, v[3] * inv);
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[(int64_t)(w.q0 + token) * p.hq + head] = finish_lse(m, l);
+    if (kShare == 1 || wave == 0) {
+      if (sub == 0 && d < p.D)
+        store4<T>((T*)p.out + (int64_t)(w.q0 + token) * p.o_token + head * p.o_head + d, v[0] * inv,
+                  v[1] * inv, v[2] * inv, v[3] * inv);
+      if (lane == 0 && p.lse != nullptr)
+        p.lse[(int64_t)(w.q0 + token) * p.hq + head] = finish_lse(m, l);
+    }
+    if constexpr (kShare == 4) __syncthreads();
   }
 }
 

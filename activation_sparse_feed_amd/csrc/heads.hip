@@ -11,6 +11,8 @@
 // walks over the token's heads.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "attn.h"
 #include "common.cuh"
 
@@ -22,36 +24,22 @@ namespace {
 template <typename T, int V> struct Chunk {
   static constexpr int kBytes = V * (int)sizeof(T);
   typedef uint32_t raw_t __attribute__((ext_vector_type(kBytes / 4)));
-  __device__ static __forceinline__ void load(const T* p, float (&o)[V]) {
-    uint32_t w[kBytes / 4];
-    if constexpr (kBytes == 4) {
-      w[0] = *(const uint32_t*)p;
-    } else {
-      const raw_t r = *(const raw_t*)p;
-#pragma unroll
-      for (int i = 0; i < kBytes / 4; ++i) w[i] = r[i];
-    }
+  __device__ static __forceinline__ void unpack(const raw_t& w, float (&o)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if constexpr (sizeof(T) == 4) o[i] = __uint_as_float(w[i]);
       else o[i] = (i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
     }
   }
+  __device__ static __forceinline__ void load(const T* p, float (&o)[V]) { unpack(*(const raw_t*)p, o); }
   __device__ static __forceinline__ void store(T* p, const float (&v)[V]) {
-    uint32_t w[kBytes / 4];
+    raw_t r;
 #pragma unroll
     for (int i = 0; i < kBytes / 4; ++i) {
-      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
-      else w[i] = (uint32_t)f32_to_bf16(v[2 * i]) | ((uint32_t)f32_to_bf16(v[2 * i + 1]) << 16);
+      if constexpr (sizeof(T) == 4) r[i] = __float_as_uint(v[i]);
+      else r[i] = (uint32_t)f32_to_bf16(v[2 * i]) | ((uint32_t)f32_to_bf16(v[2 * i + 1]) << 16);
     }
-    if constexpr (kBytes == 4) {
-      *(uint32_t*)p = w[0];
-    } else {
-      raw_t r;
-#pragma unroll
-      for (int i = 0; i < kBytes / 4; ++i) r[i] = w[i];
-      *(raw_t*)p = r;
-    }
+    *(raw_t*)p = r;
   }
 };
 
@@ -99,17 +87,29 @@ __device__ __forceinline__ Unit unit_of(int u, int D, int rot, bool adjacent) {
   return r;
 }
 
+// n floats of a row of the table, 4-byte aligned.
+template <int N>
+__device__ __forceinline__ void load_floats(const float* p, float* o) {
+  typedef float vec_t __attribute__((ext_vector_type(N < 4 ? N : 4), aligned(4)));
+  constexpr int kStep = N < 4 ? N : 4;
+#pragma unroll
+  for (int i = 0; i < N; i += kStep) {
+    const vec_t v = *(const vec_t*)(p + i);
+#pragma unroll
+    for (int j = 0; j < kStep; ++j) o[i + j] = v[j];
+  }
+}
+
 // cos and sin of a unit's pairs: for pair units V angles; for adjacent pairs
 // V / 2 angles of each chunk (1, 0 beyond rot).  A position outside the table
-// gives NaN.
+// gives NaN.  `pos` is the token's.
 template <int V>
 __device__ __forceinline__ void load_angles(const Unit& u, bool adjacent, const float* table,
-                                            int rot, int max_pos, const int32_t* positions,
-                                            int t, float (&c)[V], float (&s)[V]) {
+                                            int rot, int max_pos, int pos, float (&c)[V],
+                                            float (&s)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) c[i] = 1.f, s[i] = 0.f;
-  if (rot == 0 || !u.live) return;
-  const int pos = positions[t];
+  if (rot == 0) return;
   const bool ok = pos >= 0 && pos < max_pos;
   const float* row = table + (size_t)(ok ? pos : 0) * rot;
   const float bad = __builtin_nanf("");
@@ -117,18 +117,25 @@ __device__ __forceinline__ void load_angles(const Unit& u, bool adjacent, const 
 #pragma unroll
     for (int i = 0; i < V; ++i) {  // i < V/2: the first chunk's pairs, else the second's
       const int e = (i < V / 2 ? u.o0 : u.o1) + 2 * (i % (V / 2));
-      if ((i < V / 2 || u.o1 >= 0) && e < rot) {
-        c[i] = ok ? row[e / 2] : bad;
-        s[i] = ok ? row[rot / 2 + e / 2] : bad;
-      }
+      const bool in = e < rot && (i < V / 2 || u.o1 >= 0);
+      const int at = in ? e / 2 : 0;
+      const float ci = row[at], si = row[rot / 2 + at];
+      c[i] = !in ? 1.f : ok ? ci : bad;
+      s[i] = !in ? 0.f : ok ? si : bad;
     }
   } else if (u.pair) {
+    load_floats<V>(row + u.o0, c);
+    load_floats<V>(row + rot / 2 + u.o0, s);
+    if (!ok) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      c[i] = ok ? row[u.o0 + i] : bad;
-      s[i] = ok ? row[rot / 2 + u.o0 + i] : bad;
+      for (int i = 0; i < V; ++i) c[i] = s[i] = bad;
     }
   }
+}
+
+// The position of token t, one for the wave: a scalar load.
+__device__ __forceinline__ int position_of(const int32_t* positions, int rot, int t) {
+  return rot == 0 ? 0 : *(const __attribute__((address_space(4))) int32_t*)(positions + t);
 }
 
 // Rotation of a unit in place; `sign` -1 applies the transposed rotation.
@@ -172,16 +179,19 @@ __device__ __forceinline__ void store_unit(T* row, const Unit& u, const float (&
   if (u.live && u.o1 >= 0) Chunk<T, V>::store(row + u.o1, b);
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void load_weight(const T* w, const Unit& u, float (&a)[V],
-                                            float (&b)[V]) {
-  if (w != nullptr) {
-    load_unit<T, V>(w, u, a, b);
-  } else {
+// A unit's weights as they lie in memory (w null: ones).
+template <typename T, int V> struct RawWeight {
+  typename Chunk<T, V>::raw_t a, b;
+  __device__ __forceinline__ void load(const T* w, const Unit& u) {
+    constexpr uint32_t one = sizeof(T) == 4 ? 0x3f800000u : 0x3f803f80u;
 #pragma unroll
-    for (int i = 0; i < V; ++i) a[i] = b[i] = 1.f;
+    for (int i = 0; i < Chunk<T, V>::kBytes / 4; ++i) a[i] = b[i] = one;
+    if (w != nullptr && u.live) {
+      a = *(const typename Chunk<T, V>::raw_t*)(w + u.o0);
+      if (u.o1 >= 0) b = *(const typename Chunk<T, V>::raw_t*)(w + u.o1);
+    }
   }
-}
+};
 
 constexpr int kHeadsBlock = 256;
 
@@ -205,7 +215,12 @@ __global__ __launch_bounds__(kHeadsBlock) void heads_fwd(HeadsFwd p) {
     vc = page * p.vc_page + off * p.vc_token;
   }
   float c[V], s[V];
-  load_angles<V>(un, adjacent, p.table, p.rot, p.max_pos, p.positions, t, c, s);
+  load_angles<V>(un, adjacent, p.table, p.rot, p.max_pos, position_of(p.positions, p.rot, t), c, s);
+  RawWeight<T, V> wq, wk;
+  if (p.norm) {
+    wq.load((const T*)p.q_weight, un);
+    wk.load((const T*)p.k_weight, un);
+  }
   const int n_v = p.slots != nullptr ? p.hkv : 0;
   const int rows = p.hq + p.hkv + n_v;
   const float inv_d = 1.f / (float)p.D;
@@ -231,9 +246,10 @@ __global__ __launch_bounds__(kHeadsBlock) void heads_fwd(HeadsFwd p) {
     ss = row_sum(ss, G);
     if (is_q || is_k) {
       if (p.norm) {
-        const float rs = 1.f / sqrtf(ss * inv_d + p.eps);
+        const float rs = __builtin_amdgcn_rsqf(ss * inv_d + p.eps);  // to 1 ulp
         float wa[V], wb[V];
-        load_weight<T, V>((const T*)(is_q ? p.q_weight : p.k_weight), un, wa, wb);
+        Chunk<T, V>::unpack(is_q ? wq.a : wk.a, wa);
+        Chunk<T, V>::unpack(is_q ? wq.b : wk.b, wb);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           a[i] = a[i] * rs * wa[i];
@@ -246,71 +262,114 @@ __global__ __launch_bounds__(kHeadsBlock) void heads_fwd(HeadsFwd p) {
   }
 }
 
-// Backward: one wave walks over tokens blockwise; the weight gradients of its
-// unit stay in registers and are summed over the block's waves at the end, in
-// a fixed order, into one row of partials per block.
+// A row's part of this lane as it lies in memory, x and the gradient.
+template <typename T, int V> struct RawRow {
+  typename Chunk<T, V>::raw_t x0, x1, g0, g1;
+};
+
+// Backward: one wave walks over tokens; the weight gradients of its unit stay in
+// registers and are summed over the block's waves at the end, in a fixed order,
+// into one row of partials per block.  The next rows are loaded before a row's
+// arithmetic, so that loads are in flight all the time.
 template <typename T, int V>
 __global__ __launch_bounds__(kHeadsBlock) void heads_bwd(HeadsBwd p) {
+  typedef Chunk<T, V> C;
   const int lane = lane_id(), w = threadIdx.x / kWave;
   const int G = p.lanes_per_row, u = lane & (G - 1), sub = lane / G, rpw = kWave / G;
   const bool adjacent = p.rot_adjacent != 0;
   const Unit un = unit_of<V>(u, p.D, p.rot, adjacent);
   const float inv_d = 1.f / (float)p.D;
+  const bool has1 = un.live && un.o1 >= 0;
   float gw[2][2][V];
 #pragma unroll
   for (int i = 0; i < V; ++i) gw[0][0][i] = gw[0][1][i] = gw[1][0][i] = gw[1][1][i] = 0.f;
   const int waves = (int)gridDim.x * (kHeadsBlock / kWave);
-  for (int t = uniform((int)blockIdx.x * (kHeadsBlock / kWave) + w); t < p.T; t += waves) {
-    float c[V], s[V];
-    load_angles<V>(un, adjacent, p.table, p.rot, p.max_pos, p.positions, t, c, s);
+  RawWeight<T, V> weight[2];
+  if (p.norm) {
+    weight[0].load((const T*)p.q_weight, un);
+    weight[1].load((const T*)p.k_weight, un);
+  }
+
+  auto load = [&](int which, int t, int h0) __attribute__((always_inline)) {
+    RawRow<T, V> r = {};
+    const int h = h0 + sub;
+    if (!un.live || t >= p.T || h >= (which == 0 ? p.hq : p.hkv)) return r;
+    const T* x = (const T*)(which == 0 ? p.q : p.k) +
+                 (which == 0 ? t * p.q_token + h * p.q_head : t * p.k_token + h * p.k_head);
+    const T* g = (const T*)(which == 0 ? p.gq_out : p.gk_out) +
+                 (which == 0 ? t * p.gqo_token + h * p.gqo_head : t * p.gko_token + h * p.gko_head);
+    if (p.norm) {
+      r.x0 = *(const typename C::raw_t*)(x + un.o0);
+      if (has1) r.x1 = *(const typename C::raw_t*)(x + un.o1);
+    }
+    r.g0 = *(const typename C::raw_t*)(g + un.o0);
+    if (has1) r.g1 = *(const typename C::raw_t*)(g + un.o1);
+    return r;
+  };
+  auto process = [&](auto which_c, const RawRow<T, V>& raw, int t, int h0, const float (&c)[V],
+                     const float (&s)[V]) __attribute__((always_inline)) {
+    constexpr int which = decltype(which_c)::value;
+    const int h = h0 + sub, heads = which == 0 ? p.hq : p.hkv;
+    Unit me = un;
+    me.live = me.live && h < heads;
+    float ga[V], gb[V];
+    C::unpack(raw.g0, ga);
+    C::unpack(raw.g1, gb);
+    rotate<V>(un, adjacent, c, s, -1.f, ga, gb);
+    if (p.norm) {
+      float wa[V], wb[V], a[V], b[V];
+      C::unpack(weight[which].a, wa);
+      C::unpack(weight[which].b, wb);
+      C::unpack(raw.x0, a);
+      C::unpack(raw.x1, b);
+      float ss = 0.f, dot = 0.f;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {  // q, then k
-      const int heads = which == 0 ? p.hq : p.hkv;
-      const T* x = (const T*)(which == 0 ? p.q : p.k);
-      const int64_t xt = which == 0 ? p.q_token : p.k_token, xh = which == 0 ? p.q_head : p.k_head;
-      const T* gy = (const T*)(which == 0 ? p.gq_out : p.gk_out);
-      const int64_t yt = which == 0 ? p.gqo_token : p.gko_token,
-                    yh = which == 0 ? p.gqo_head : p.gko_head;
-      T* gx = (T*)(which == 0 ? p.gq : p.gk);
-      const int64_t gt = which == 0 ? p.gq_token : p.gk_token,
-                    gh = which == 0 ? p.gq_head : p.gk_head;
-      float wa[V], wb[V];
-      load_weight<T, V>((const T*)(which == 0 ? p.q_weight : p.k_weight), un, wa, wb);
-      for (int h0 = 0; h0 < heads; h0 += rpw) {
-        const int h = h0 + sub;
-        Unit me = un;
-        me.live = me.live && h < heads;
-        float ga[V], gb[V];
-        load_unit<T, V>(gy + t * yt + h * yh, me, ga, gb);
-        rotate<V>(un, adjacent, c, s, -1.f, ga, gb);
-        if (p.norm) {
-          float a[V], b[V];
-          load_unit<T, V>(x + t * xt + h * xh, me, a, b);
-          float ss = 0.f, dot = 0.f;
+      for (int i = 0; i < V; ++i) {
+        ss += a[i] * a[i] + b[i] * b[i];
+        dot += ga[i] * wa[i] * a[i] + gb[i] * wb[i] * b[i];
+      }
+      ss = row_sum(ss, G);
+      dot = row_sum(dot, G);
+      const float rs = __builtin_amdgcn_rsqf(ss * inv_d + p.eps);  // to 1 ulp
+      const float m = dot * rs * inv_d;  // mean of (gn w) xhat
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            ss += a[i] * a[i] + b[i] * b[i];
-            dot += ga[i] * wa[i] * a[i] + gb[i] * wb[i] * b[i];
-          }
-          ss = row_sum(ss, G);
-          dot = row_sum(dot, G);
-          const float rs = 1.f / sqrtf(ss * inv_d + p.eps);
-          const float m = dot * rs * inv_d;  // mean of (gn w) xhat
-          const bool add = h < heads;
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float ha = a[i] * rs, hb = b[i] * rs;
-            if (add) {
-              gw[which][0][i] += ga[i] * ha;
-              gw[which][1][i] += gb[i] * hb;
-            }
-            ga[i] = rs * (ga[i] * wa[i] - ha * m);
-            gb[i] = rs * (gb[i] * wb[i] - hb * m);
-          }
+      for (int i = 0; i < V; ++i) {
+        const float ha = a[i] * rs, hb = b[i] * rs;
+        if (h < heads) {
+          gw[which][0][i] += ga[i] * ha;
+          gw[which][1][i] += gb[i] * hb;
         }
-        store_unit<T, V>(gx + t * gt + h * gh, me, ga, gb);
+        ga[i] = rs * (ga[i] * wa[i] - ha * m);
+        gb[i] = rs * (gb[i] * wb[i] - hb * m);
       }
     }
+    T* gx = which == 0 ? (T*)p.gq + t * p.gq_token + h * p.gq_head : (T*)p.gk + t * p.gk_token + h * p.gk_head;
+    store_unit<T, V>(gx, me, ga, gb);
+  };
+
+  int t = uniform((int)blockIdx.x * (kHeadsBlock / kWave) + w);
+  float c[V], s[V];
+  RawRow<T, V> row = load(p.hq > 0 ? 0 : 1, t, 0);
+  if (t < p.T) load_angles<V>(un, adjacent, p.table, p.rot, p.max_pos, position_of(p.positions, p.rot, t), c, s);
+  for (; t < p.T; t += waves) {
+    const int tn = t + waves;
+    const int pos_next = position_of(p.positions, p.rot, min(tn, p.T - 1));
+    float cn[V], sn[V];
+    for (int h0 = 0; h0 < p.hq; h0 += rpw) {
+      const bool more = h0 + rpw < p.hq, k = p.hkv > 0;
+      const RawRow<T, V> next = load(more || !k ? 0 : 1, more || k ? t : tn, more ? h0 + rpw : 0);
+      process(std::integral_constant<int, 0>{}, row, t, h0, c, s);
+      row = next;
+    }
+    load_angles<V>(un, adjacent, p.table, p.rot, p.max_pos, pos_next, cn, sn);
+    for (int h0 = 0; h0 < p.hkv; h0 += rpw) {
+      const bool more = h0 + rpw < p.hkv, q = p.hq > 0;
+      const RawRow<T, V> next = load(more || !q ? 1 : 0, more ? t : tn, more ? h0 + rpw : 0);
+      process(std::integral_constant<int, 1>{}, row, t, h0, c, s);
+      row = next;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = cn[i], s[i] = sn[i];
   }
   if (p.partial == nullptr) return;
   // sum over the rows a wave holds side by side, then over the block's waves

@@ -130,7 +130,7 @@ hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipS
     if (e != hipSuccess) return e;
     if (keys.splits > 1) {
       const int64_t most = (int64_t)p.max_q * a.g < kKeysTile ? (int64_t)p.max_q * a.g : kKeysTile;
-      const unsigned join_y = (unsigned)((most + 3) / 4);  // a wave for every row
+      const unsigned join_y = (unsigned)most;  // a workgroup for every row
       hipLaunchKernelGGL((attn_join<T, kKeysTile>), dim3((unsigned)(keys.tiles * p.hkv), join_y), dim3(256),
                          0, s, a);
       e = hipGetLastError();
