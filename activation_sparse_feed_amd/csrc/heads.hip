@@ -438,7 +438,7 @@ int lanes_per_row(int D, int rot, bool adjacent, int V) {
 // Blocks of the backward: enough waves to fill the GPU, few enough partials.
 int bwd_blocks(int T) {
   const int need = (T + kHeadsBlock / kWave - 1) / (kHeadsBlock / kWave);
-  return need < 1024 ? need : 1024;
+  return need < 512 ? need : 512;
 }
 
 template <template <typename, int> class F, typename P>
