@@ -267,9 +267,10 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
     load_v.look_up(j0 + KT);
     load_k.start(k0);
     load_k.look_up(j0 + KT + 32);
-    tile.load_q(q, p.D, a.negate != 0);
+    tile.load_q(q, p.D);
     wait_loads<0>();
     __syncthreads();
+    if (a.negate) tile.negate();
     s = tile.scores(k1 + KT * Tile::kPitch - Tile::kBlockBytes);
   }
   auto iteration = [&](uint8_t* k, uint8_t* v, uint8_t* k_next, uint8_t* v_next) __attribute__((always_inline)) {
@@ -343,18 +344,21 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
 }
 
 template <typename T, int DP, int NW, int G, bool COMPACT>
-__global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
+__global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys(AttnArgs a) {
   constexpr int KT = 32;
   typedef AttnTile<T, DP, KT> Tile;
-  __shared__ __align__(1024) uint8_t k0[NW][Tile::kTileBytes], k1[NW][Tile::kTileBytes],
-      v0[NW][Tile::kTileBytes], v1[NW][Tile::kTileBytes];
+  __shared__ __align__(1024) uint8_t k_lds[NW][Tile::kTileBytes], v_lds[NW][Tile::kTileBytes];
   __shared__ float ml[NW][32][2];
   const PagedAttn& p = a.p;
   const int wave = uniform((int)threadIdx.x / kWave), lane = lane_id(), half = lane >> 5;
-  if (p.D != DP)  // chunks that are read, but that no load writes
+  uint8_t *const k = k_lds[wave], *const v = v_lds[wave];
+  auto clear = [&]() __attribute__((always_inline)) {  // chunks that are read, but that no load writes
+    if (p.D == DP) return;
     for (int i = lane * 16; i < Tile::kTileBytes; i += kWave * 16)
-      *(u32x4_t*)(k0[wave] + i) = *(u32x4_t*)(k1[wave] + i) = *(u32x4_t*)(v0[wave] + i) =
-          *(u32x4_t*)(v1[wave] + i) = u32x4_t{0u, 0u, 0u, 0u};
+      *(u32x4_t*)(k + i) = *(u32x4_t*)(v + i) = u32x4_t{0u, 0u, 0u, 0u};
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): written
+  };
+  clear();
   // Items (sequence, tile, split) are numbered from bounds of the lengths: the item of
   // a workgroup is at hand, but may not exist.  A workgroup without work still waits
   // for its place in LDS, so where most are expected to be of that kind (COMPACT:
@@ -394,51 +398,65 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
     tile.init();
     TileLoader<T, DP, KT, G, Tile::kLoads, true> load_k;
     TileLoader<T, DP, KT, G, Tile::kLoads, false> load_v;
+    // All but the newest tile's loads are done.  Every tile is kLoads of them (a
+    // wave-wide load has lanes within head_dim); with page lookups among the loads
+    // their order is the compiler's, so all are waited for.
+    auto wait_one = [&]() __attribute__((always_inline)) {
+      if constexpr (G > 0) wait_loads<Tile::kLoads>();
+      else wait_loads<0>();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    };
     load_k.init(a, w.seq, hk, b, e, 0);
     load_v.init(a, w.seq, hk, b, e, 0);
     int j0 = (b & ~(KT - 1)) + wave * KT;
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // the zeros are written (lgkmcnt)
-    auto load = [&](int j, uint8_t* k, uint8_t* v) __attribute__((always_inline)) {
-      load_k.start(k);
-      load_v.start(v);
-      load_k.look_up(j + NW * KT);
-      load_v.look_up(j + NW * KT);
-    };
-    if (b < e && j0 < e) {
+    const int end = b < e ? e : j0;  // nothing to do: no iteration
+    if (j0 < end) {
       load_k.look_up(j0);
       load_v.look_up(j0);
-      load(j0, k0[wave], v0[wave]);
-      tile.load_q((const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D, a.negate != 0);
+      tile.load_q((const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D);
+      load_k.start(k);
+      load_v.start(v);
+      load_k.look_up(j0 + NW * KT);
+      load_v.look_up(j0 + NW * KT);
+      wait_one();
+      if (a.negate) tile.negate();
     }
-    auto iteration = [&](uint8_t* k, uint8_t* v, uint8_t* k_next, uint8_t* v_next) __attribute__((always_inline)) {
-      wait_loads<0>();
-      __builtin_amdgcn_wave_barrier();
+    // One tile each of K and V: the next K is loaded as soon as the scores have read
+    // this one, the next V after the product, so that one of them is always in flight.
+    for (; j0 < end; j0 += NW * KT) {
+      const bool more = j0 + NW * KT < end, whole = j0 >= x && j0 + KT <= y;
+      wait_one();  // K is here
+      f32x16_t s = tile.scores(k);
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): it has been read
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) {
+        load_k.start(k);
+        load_k.look_up(j0 + 2 * NW * KT);
+      }
+      if (!whole) Tile::hide(s, j0, row_lo, row_hi);
+      tile.raise(s, a.c);
+      tile.weights(s, a.c);
+      if (more) wait_one();  // V is here
+      else wait_loads<0>();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      if (j0 + NW * KT < e) load(j0 + NW * KT, k_next, v_next);
-      const bool whole = j0 >= x && j0 + KT <= y;
       if (!whole && __any(Tile::template find_infinite<kWave>(v, lane))) {
         tile.add_infinite(v, j0, row_lo, row_hi);
         Tile::template clear_infinite<kWave>(v, lane);
       }
-      f32x16_t s = tile.scores(k);
-      if (!whole) Tile::hide(s, j0, row_lo, row_hi);
-      tile.raise(s, a.c);
-      tile.weights(s, a.c);
       tile.accumulate(v, s);
-      j0 += NW * KT;
-    };
-    while (b < e && j0 < e) {
-      iteration(k0[wave], v0[wave], k1[wave], v1[wave]);
-      if (j0 >= e) break;
-      iteration(k1[wave], v1[wave], k0[wave], v0[wave]);
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) {
+        load_v.start(v);
+        load_v.look_up(j0 + 2 * NW * KT);
+      }
     }
     tile.l = sum_halves(tile.l);
-    // Join the waves: each leaves its rows in its V arrays (K's must keep the zeros of
-    // chunks beyond head_dim), 32 x 32 floats for each block of 32 outputs, row r's
-    // 16-byte chunk c at c ^ (r % 8).
+    // Join the waves: each leaves its rows in its LDS, 32 x 32 floats for each block of
+    // 32 outputs, row r's 16-byte chunk c at c ^ (r % 8).
     constexpr int kPerArray = Tile::kTileBytes / 4096;
     static_assert(kPerArray * 2 >= Tile::kDt, "");
-    auto part = [&](int wv, int d) { return (d < kPerArray ? v0[wv] + d * 4096 : v1[wv] + (d - kPerArray) * 4096); };
+    auto part = [&](int wv, int d) { return (d < kPerArray ? v_lds[wv] + d * 4096 : k_lds[wv] + (d - kPerArray) * 4096); };
     {
       const int row = lane & 31;
 #pragma unroll
@@ -485,7 +503,9 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys(AttnArgs a) {
       }
     }
     if constexpr (!COMPACT) break;
+    wait_loads<0>();   // the outputs are written (they count among the loads)
     __syncthreads();  // the waves' results are read before the next item's tiles arrive
+    clear();
   }
 }
 
@@ -577,11 +597,10 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
 
 constexpr int kCus = 256;
 
-// Waves of an attn_keys workgroup: as many as the LDS of a CU holds tiles for (four
-// tiles of 32 rows a wave, of 64, 128 or 256 elements), at most 8.
+// Waves of an attn_keys workgroup: tiles of K and V (32 rows of 64, 128 or 256 elements)
+// for all of them in 64 KB, so that two workgroups share a CU.
 constexpr int attn_keys_waves(int elt_bytes, int head_dim) {
-  const int tiles = 4 * 32 * (head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256) * elt_bytes;
-  return tiles <= (16 << 10) ? 8 : tiles <= (32 << 10) ? 4 : tiles <= (64 << 10) ? 2 : 1;
+  return (64 << 10) / (2 * 32 * (head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256) * elt_bytes);
 }
 
 // Launches of one element type, in files of their own.

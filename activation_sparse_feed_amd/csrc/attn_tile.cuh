@@ -144,16 +144,20 @@ struct AttnTile {
     l = 0.f;
   }
 
-  // This lane's part of query row `row` (B operand: chunks 2 i + lane / 32).
-  __device__ __forceinline__ void load_q(const T* row, int D, bool negate) {
+  // This lane's part of query row `row` (B operand: chunks 2 i + lane / 32).  A negative
+  // scale is applied by negate(), once the loads are done.
+  __device__ __forceinline__ void load_q(const T* row, int D) {
     const int h = lane_id() >> 5;
 #pragma unroll
     for (int i = 0; i < kQ; ++i) {
       const int e = (2 * i + h) * kEpc;
-      u32x4_t v = {0u, 0u, 0u, 0u};
-      if (e < D) v = ldg16(row + e);
-      q[i] = negate ? Frag<T>::negate(v) : v;
+      q[i] = u32x4_t{0u, 0u, 0u, 0u};
+      if (e < D) q[i] = ldg16(row + e);
     }
+  }
+  __device__ __forceinline__ void negate() {
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) q[i] = Frag<T>::negate(q[i]);
   }
 
   // S^T of the 32 keys at `k`.
