@@ -68,10 +68,16 @@ Plan plan_keys(int dtype, const PagedAttn& p) {
   pl.part_rows = (size_t)pl.tiles * p.hkv * kKeysTile;
   // A wave takes about 1 us for 32 keys (3 us in float32, whose products are 16 times
   // slower), the join and its launch 5 us: ranges of up to 8 (2) steps a wave
-  // are not split, longer ones into at least half of that.
-  const int steps = attn_keys_waves(dtype == 1 ? 2 : 4, p.D) * 32 * (dtype == 1 ? 8 : 2);
+  // are not split.  Longer ones into chunks of 2 (1) to 6 (1) steps: 6 even out
+  // ragged lengths better than 8 (32 tokens over up to 4096 keys 67.8 -> 63.8 us),
+  // fewer spread a few long ranges over the GPU.
+  const int step = attn_keys_waves(dtype == 1 ? 2 : 4, p.D) * 32;
+  const int whole = step * (dtype == 1 ? 8 : 2);
   const int64_t span = key_span(p, kKeysMax / g + 1);
-  split(&pl, p, span, (int64_t)pl.tiles * p.hkv, 4 * kCus, span <= steps ? steps : steps / 2, steps);
+  if (span <= whole) split(&pl, p, span, 1, 1, whole, whole);
+  else
+    split(&pl, p, span, (int64_t)pl.tiles * p.hkv, 4 * kCus, step * (dtype == 1 ? 2 : 1),
+          step * (dtype == 1 ? 6 : 1));
   return pl;
 }
 
