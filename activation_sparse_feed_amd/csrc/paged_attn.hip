@@ -59,20 +59,22 @@ void split(Plan* pl, const PagedAttn& p, int64_t span, int64_t groups, int64_t w
 Plan plan_keys(int dtype, const PagedAttn& p) {
   Plan pl = {};
   const int64_t g = p.hq / p.hkv, rows = p.max_q * g;
-  // a single sequence with more rows than fit goes to attn_rows alone
-  pl.used = p.n_seqs > 1 ? g <= kKeysMax : rows <= kKeysMax;
+  // where every sequence has max_q tokens and so more rows than fit, attn_rows takes
+  // them all
+  const bool equal = p.T == (int64_t)p.n_seqs * p.max_q;
+  pl.used = g <= kKeysMax && (rows <= kKeysMax || !equal);
   if (!pl.used) return pl;
   pl.max_rows = kKeysMax;
   pl.tiles_per_seq = (int)(((rows < kKeysMax ? rows : kKeysMax) + kKeysTile - 1) / kKeysTile);
   pl.tiles = p.n_seqs * pl.tiles_per_seq;
   pl.part_rows = (size_t)pl.tiles * p.hkv * kKeysTile;
-  // A wave takes about 1 us for 32 keys (3 us in float32, whose products are 16 times
-  // slower), the join and its launch 5 us: ranges of up to 8 (2) steps a wave
+  // A wave takes 1 to 2 us for 32 keys (3 us in float32, whose products are 16 times
+  // slower), the join and its launch 6 us: ranges of up to 5 (2) steps a wave
   // are not split.  Longer ones into chunks of 2 (1) to 6 (1) steps: 6 even out
   // ragged lengths better than 8 (32 tokens over up to 4096 keys 67.8 -> 63.8 us),
   // fewer spread a few long ranges over the GPU.
   const int step = attn_keys_waves(dtype == 1 ? 2 : 4, p.D) * 32;
-  const int whole = step * (dtype == 1 ? 8 : 2);
+  const int whole = step * (dtype == 1 ? 5 : 2);
   const int64_t span = key_span(p, kKeysMax / g + 1);
   if (span <= whole) split(&pl, p, span, 1, 1, whole, whole);
   else
@@ -91,10 +93,10 @@ Plan plan_rows(int dtype, const PagedAttn& p, bool with_keys) {
   // every taken sequence has at most one tile that is not full
   int64_t part = rows / (pl.min_rows + 1);
   if (part > p.n_seqs) part = p.n_seqs;
-  pl.tiles = (int)(rows / kRowsTile + part);
+  pl.tiles = (int)((rows + part * (kRowsTile - 1)) / kRowsTile);
   pl.part_rows = (size_t)pl.tiles * p.hkv * kRowsTile;
   split(&pl, p, key_span(p, kRowsTile / g + 2), (int64_t)pl.tiles * p.hkv, 2 * kCus,
-        dtype == 1 ? 512 : 128, 1 << 30);
+        dtype == 1 ? 256 : 128, 1 << 30);
   return pl;
 }
 
@@ -110,6 +112,13 @@ void place(AttnArgs* a, const Plan& pl, void* ws) {
   a->part_ml = (float*)((char*)ws + align256((size_t)pl.splits * pl.part_rows * a->p.D * 4));
 }
 
+// Workgroups of a join: for every tile up to y (one for each step over its rows), but
+// not many more than `most`, since each first finds out which rows are its own.
+dim3 join_grid(int tiles, int y, int most) {
+  const int fit = most / tiles < 1 ? 1 : most / tiles;
+  return dim3((unsigned)tiles, (unsigned)(y < fit ? y : fit));
+}
+
 template <typename T>
 hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipStream_t s) {
   const PagedAttn& p = a.p;
@@ -123,7 +132,7 @@ hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipS
     e = launch_attn_rows<T>(a, granule, s);
     if (e != hipSuccess) return e;
     if (rows.splits > 1) {
-      hipLaunchKernelGGL((attn_join<T, kRowsTile>), dim3((unsigned)(rows.tiles * p.hkv), 32),
+      hipLaunchKernelGGL((attn_join<T, kRowsTile>), join_grid(rows.tiles * p.hkv, kRowsTile / 4, 1024),
                          dim3(256), 0, s, a);
       e = hipGetLastError();
       if (e != hipSuccess) return e;
@@ -135,9 +144,8 @@ hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipS
     e = launch_attn_keys<T>(a, granule, rows.used, s);
     if (e != hipSuccess) return e;
     if (keys.splits > 1) {
-      const int64_t most = (int64_t)p.max_q * a.g < kKeysTile ? (int64_t)p.max_q * a.g : kKeysTile;
-      const unsigned join_y = (unsigned)most;  // a workgroup for every row
-      hipLaunchKernelGGL((attn_join<T, kKeysTile>), dim3((unsigned)(keys.tiles * p.hkv), join_y), dim3(256),
+      const int most = (int64_t)p.max_q * a.g < kKeysTile ? p.max_q * a.g : kKeysTile;
+      hipLaunchKernelGGL((attn_join<T, kKeysTile>), join_grid(keys.tiles * p.hkv, most, 4096), dim3(256),
                          0, s, a);
       e = hipGetLastError();
     }
