@@ -544,6 +544,48 @@ def paged_attn_fwd(batch: PagedBatch, q, k_cache, v_cache, q_start, kv_len, bloc
         _stream_ptr(stream)))
 
 
+def paged_slots(block_table, seq, positions, page_size: int) -> torch.Tensor:
+    """Slots (int32) of tokens at `positions` of the sequences `seq`, through
+    block_table; computed once a step, for all layers."""
+    pos = positions.long()
+    page = block_table[seq.long(), pos // page_size].long()
+    return (page * page_size + pos % page_size).to(torch.int32)
+
+
+class PagedAttention:
+    """Cache and buffers of one layer for repeated serving steps of one batch
+    shape (T new tokens of n_seqs sequences).  ``forward`` issues paged_kv_append
+    and paged_attn_fwd on one stream with no host synchronisation.  The caches
+    may be given (``k_cache``, ``v_cache``), e.g. to use them with several batch
+    shapes."""
+
+    def __init__(self, T: int, n_seqs: int, n_q_heads: int, n_kv_heads: int, head_dim: int, dtype,
+                 page_size: int, n_pages: int, max_pages: int, max_q: int, max_kv: int,
+                 rot_dim: int = 0, max_pos: int = 0, norm: bool = False, eps: float = 1e-6,
+                 adjacent: bool = False, causal: bool = True, window: int = 0,
+                 scale: float | None = None, k_cache=None, v_cache=None, device="cuda"):
+        self.heads = make_heads(T, n_q_heads, n_kv_heads, head_dim, dtype, rot_dim, max_pos, norm,
+                                eps, adjacent)
+        self.batch = make_paged_batch(T, n_seqs, n_q_heads, n_kv_heads, head_dim, dtype, page_size,
+                                      n_pages, max_pages, max_q, max_kv, causal, window, scale)
+        dt = _TORCH_DTYPE[self.heads.dtype]
+        shape = (n_pages, page_size, n_kv_heads, head_dim)
+        self.k_cache = torch.empty(shape, dtype=dt, device=device) if k_cache is None else k_cache
+        self.v_cache = torch.empty(shape, dtype=dt, device=device) if v_cache is None else v_cache
+        self.q_out = torch.empty((T, n_q_heads, head_dim), dtype=dt, device=device)
+        self.out = torch.empty((T, n_q_heads, head_dim), dtype=dt, device=device)
+        self.lse = torch.empty((T, n_q_heads), dtype=torch.float32, device=device)
+        self.workspace = alloc_paged_workspace(self.batch, device)
+
+    def forward(self, q, k, v, positions, slots, q_start, kv_len, block_table, table=None,
+                q_weight=None, k_weight=None, stream=None) -> torch.Tensor:
+        paged_kv_append(self.heads, q, k, v, q_weight, k_weight, table, positions, slots,
+                        self.q_out, self.k_cache, self.v_cache, stream)
+        paged_attn_fwd(self.batch, self.q_out, self.k_cache, self.v_cache, q_start, kv_len,
+                       block_table, self.out, self.workspace, self.lse, stream)
+        return self.out
+
+
 class SparseFFN:
     """Buffers for repeated sparse forwards of one shape: TwELL arrays, routed
     list, workspaces.  ``forward`` issues twell_pack, sparse_ffn_fwd and
