@@ -28,15 +28,18 @@ struct Work {
   int seq, q0, nq, nkv, tile;  // tile < 0: none
 };
 
-__device__ __forceinline__ void read_sequence(const PagedAttn& p, int s, Work* w) {
-  s = uniform(s);
-  const int q0 = load_uniform(p.q_start + s), q1 = load_uniform(p.q_start + s + 1);
-  const int len = load_uniform(p.kv_len + s);
-  const int a = min(max(q0, 0), p.T), b = min(max(q1, a), p.T);
-  w->seq = s;
-  w->q0 = a;
-  w->nq = b - a;
+// Its rows and keys from q_start[s], q_start[s + 1] and kv_len[s], within the bounds
+// that the host knows: whatever these hold, no row, key or split beyond them is used.
+__device__ __forceinline__ void bound_sequence(const PagedAttn& p, int q0, int q1, int len, Work* w) {
+  w->q0 = min(max(q0, 0), p.T);
+  w->nq = min(min(max(q1, w->q0), p.T) - w->q0, p.max_q);
   w->nkv = min(max(len, 0), p.max_kv);
+}
+
+__device__ __forceinline__ void read_sequence(const PagedAttn& p, int s, Work* w) {
+  w->seq = uniform(s);
+  bound_sequence(p, load_uniform(p.q_start + w->seq), load_uniform(p.q_start + w->seq + 1),
+                 load_uniform(p.kv_len + w->seq), w);
 }
 
 // Row tile number `t` of the sequences with more than min_rows rows.  Among 64
@@ -53,10 +56,11 @@ __device__ __forceinline__ Work find_tile(const AttnArgs& a, int t) {
     const int s = s0 + lane_id();
     int n = 0, len = -1;
     if (s < p.n_seqs) {
-      const int b = min(max(p.q_start[s], 0), p.T), e = min(max(p.q_start[s + 1], b), p.T);
-      const int rows = (e - b) * a.g;
+      Work x;
+      bound_sequence(p, p.q_start[s], p.q_start[s + 1], p.kv_len[s], &x);
+      const int rows = x.nq * a.g;
       n = rows > a.min_rows ? (rows + TM - 1) / TM : 0;
-      len = p.kv_len[s];
+      len = x.nkv;
     }
     // tiles of the sequences before this one, and of all
     int before = 0, all = 0;
@@ -141,12 +145,7 @@ struct KeysItems {
     n = 0;
     k.w.seq = s;
     k.w.q0 = k.w.nq = k.w.nkv = 0;
-    if (s < p.n_seqs) {
-      const int b = min(max(p.q_start[s], 0), p.T), e = min(max(p.q_start[s + 1], b), p.T);
-      k.w.q0 = b;
-      k.w.nq = e - b;
-      k.w.nkv = min(max(p.kv_len[s], 0), p.max_kv);
-    }
+    if (s < p.n_seqs) bound_sequence(p, p.q_start[s], p.q_start[s + 1], p.kv_len[s], &k.w);
     const int rows = k.w.nq * a.g;
     sequence_range(a, &k);
     if (rows > 0 && rows <= a.max_rows) n = (rows + 31) / 32 * k.n_split;

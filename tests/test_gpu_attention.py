@@ -359,6 +359,85 @@ def test_attention(q_lens, kv_lens, hq, hkv, D, page, dtype, causal, window, ord
     assert torch.equal(out, again)
 
 
+MORE = [
+    # many splits, and a split range that ends inside a chunk
+    ([1], [9001], 4, 1, 128, 16, "bf16", True, 0, "token"),
+    ([2, 1], [7000, 3000], 6, 2, 256, 8, "bf16", True, 0, "head"),
+    ([1, 3], [2500, 1111], 4, 4, 64, 24, "f32", True, 0, "token"),
+    ([1], [1500], 2, 1, 256, 32, "f32", True, 0, "token"),
+    # chunks over long ranges: row tiles whose keys are split, with and without a window
+    ([100], [3000], 4, 2, 128, 16, "bf16", True, 0, "token"),
+    ([90, 40], [2800, 1900], 4, 1, 64, 7, "bf16", True, 700, "token"),
+    ([130], [2000], 3, 1, 96, 16, "bf16", False, 900, "token"),
+    ([70], [1300], 2, 2, 128, 1, "f32", True, 500, "head"),
+    # windows for few rows, split and not
+    ([4, 1, 3], [5000, 900, 2100], 8, 2, 128, 16, "bf16", True, 1500, "token"),
+    ([7, 2], [400, 800], 8, 1, 64, 16, "bf16", False, 60, "token"),
+    # group sizes that divide no tile, and 33 to 64 rows (two tiles of few rows)
+    ([9, 5, 1], [900, 30, 2000], 7, 1, 128, 16, "bf16", True, 0, "token"),
+    ([13, 200], [700, 1000], 15, 3, 80, 16, "bf16", True, 0, "token"),
+    ([3], [50], 66, 1, 64, 16, "bf16", True, 0, "token"),
+    ([2, 1], [300, 70], 100, 1, 32, 16, "f32", True, 0, "token"),
+]
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,hq,hkv,D,page,dtype,causal,window,order", MORE)
+def test_attention_splits_and_groups(q_lens, kv_lens, hq, hkv, D, page, dtype, causal, window, order):
+    test_attention(q_lens, kv_lens, hq, hkv, D, page, dtype, causal, window, order)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n_seqs,long", [(70, 0), (150, 5), (300, 0), (65, 65)])
+def test_many_sequences(dtype, n_seqs, long):
+    """More sequences than a wave has lanes, chunks among single tokens, empty ones."""
+    rng = np.random.default_rng(n_seqs)
+    q_lens = [1] * n_seqs
+    for i in rng.permutation(n_seqs)[:long]:
+        q_lens[i] = int(rng.integers(20, 60))
+    kv_lens = [int(rng.integers(q, 300)) for q in q_lens]
+    for i in (0, n_seqs // 2, n_seqs - 1):
+        q_lens[i] = 0
+    c = _attention_case(q_lens, kv_lens, 8, 2, 64, 16, dtype, seed=n_seqs)
+    out, lse = _run(c)
+    _check_attention(c, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_padding_rows_are_left_alone(dtype):
+    """Rows of q past the last sequence, as in a batch padded to a fixed size."""
+    c = _attention_case([3, 80, 30], [100, 90, 50], 4, 2, 64, 16, dtype, seed=21)
+    c["qs"], c["kv"], c["bt"] = c["qs"][:3].copy(), c["kv"][:2].copy(), c["bt"][:2].copy()
+    T, B, hq, hkv, D = c["dims"]
+    c["dims"] = (T, 2, hq, hkv, D)
+    out, lse = _run(c)
+    _check_attention(c, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_wrong_lengths_and_pages_stay_in_bounds(dtype):
+    """Lengths beyond the stated bounds, rows out of range and pages that do not exist
+    are cut to the bounds (so nothing outside the buffers is touched), and the
+    sequences beside them come out right."""
+    lens = ([1, 1, 40, 1, 90], [200, 64, 300, 90, 150])
+    c = _attention_case(*lens, 4, 2, 64, 16, dtype, seed=22)
+    T, B, hq, hkv, D = c["dims"]
+    good, good_l = _run(c)
+    bad = dict(c, kv=c["kv"].copy(), qs=c["qs"].copy(), bt=c["bt"].copy())
+    bad["kv"][1] = 1 << 30
+    bad["kv"][3] = -5
+    bad["bt"][2, :3] = [1 << 30, -7, c["n_pages"]]
+    out, lse = _run(bad, max_kv=300)
+    keep = [i for b in (0, 4) for i in range(c["qs"][b], c["qs"][b + 1])]
+    assert torch.equal(out[keep], good[keep]) and torch.equal(lse[keep], good_l[keep])
+    # the sequence of negative length is empty
+    empty = int(c["qs"][3])
+    assert (out[empty] == 0).all() and torch.isneginf(lse[empty]).all()
+    # rows out of range: the last sequence starts before its neighbour ends
+    bad = dict(c, qs=c["qs"].copy())
+    bad["qs"][1:] = [-3, 1 << 30, 10, 43, 2000]
+    _run(bad, max_q=90)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("max_q,max_kv", [(100, 512), (1000, 100 * 16)])
 def test_bounds_of_the_lengths_are_upper_bounds(dtype, max_q, max_kv):
