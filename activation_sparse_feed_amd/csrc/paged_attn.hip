@@ -15,7 +15,6 @@ namespace {
 
 constexpr int kRowsTile = 128;  // rows of an attn_rows workgroup
 constexpr int kKeysTile = 32;   // rows of an attn_keys workgroup
-constexpr int kKeysMax = 64;    // rows of a sequence that attn_keys takes
 constexpr int kMaxSplits = 64;  // lanes of the join
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -26,6 +25,17 @@ struct Plan {
   int tiles, tiles_per_seq, min_rows, max_rows, chunk, splits;
   size_t part_rows, bytes;
 };
+
+// Rows of a sequence up to which attn_keys takes it: two tiles where that covers the
+// whole batch, so that attn_rows does not run (drafts of up to 5 tokens in a window,
+// 8 heads a key head: 13 us, with one tile and attn_rows beside it 31; 16 sequences of
+// up to 16 tokens, 4 heads: 38 and 49); otherwise one, since two tiles read the keys
+// twice and attn_rows runs in any case (64 sequences of up to 17 tokens: 61 us, with
+// two tiles 92; 16 of up to 40: 65 and 72; 8 of up to 30, 48 heads: 37 and 52; but 8 of
+// up to 20 over up to 20000 keys: 142 and 132).
+int keys_max(const PagedAttn& p) {
+  return p.max_q * (int64_t)(p.hq / p.hkv) <= 2 * kKeysTile ? 2 * kKeysTile : kKeysTile;
+}
 
 // Keys that the rows of one tile of at most `tokens` tokens can see.
 int64_t key_span(const PagedAttn& p, int64_t tokens) {
@@ -59,13 +69,14 @@ void split(Plan* pl, const PagedAttn& p, int64_t span, int64_t groups, int64_t w
 Plan plan_keys(int dtype, const PagedAttn& p) {
   Plan pl = {};
   const int64_t g = p.hq / p.hkv, rows = p.max_q * g;
+  const int limit = keys_max(p);
   // where every sequence has max_q tokens and so more rows than fit, attn_rows takes
   // them all
   const bool equal = p.T == (int64_t)p.n_seqs * p.max_q;
-  pl.used = g <= kKeysMax && (rows <= kKeysMax || !equal);
+  pl.used = g <= limit && (rows <= limit || !equal);
   if (!pl.used) return pl;
-  pl.max_rows = kKeysMax;
-  pl.tiles_per_seq = (int)(((rows < kKeysMax ? rows : kKeysMax) + kKeysTile - 1) / kKeysTile);
+  pl.max_rows = limit;
+  pl.tiles_per_seq = (int)(((rows < limit ? rows : limit) + kKeysTile - 1) / kKeysTile);
   pl.tiles = p.n_seqs * pl.tiles_per_seq;
   pl.part_rows = (size_t)pl.tiles * p.hkv * kKeysTile;
   // A wave takes 1 to 2 us for 32 keys (3 us in float32, whose products are 16 times
@@ -75,7 +86,7 @@ Plan plan_keys(int dtype, const PagedAttn& p) {
   // fewer spread a few long ranges over the GPU.
   const int step = attn_keys_waves(dtype == 1 ? 2 : 4, p.D) * 32;
   const int whole = step * (dtype == 1 ? 5 : 2);
-  const int64_t span = key_span(p, kKeysMax / g + 1);
+  const int64_t span = key_span(p, limit / g + 1);
   if (span <= whole) split(&pl, p, span, 1, 1, whole, whole);
   else
     split(&pl, p, span, (int64_t)pl.tiles * p.hkv, 4 * kCus, step * (dtype == 1 ? 2 : 1),
@@ -86,7 +97,7 @@ Plan plan_keys(int dtype, const PagedAttn& p) {
 Plan plan_rows(int dtype, const PagedAttn& p, bool with_keys) {
   Plan pl = {};
   const int64_t g = p.hq / p.hkv;
-  pl.min_rows = with_keys ? kKeysMax : 0;
+  pl.min_rows = with_keys ? keys_max(p) : 0;
   pl.used = p.max_q * g > pl.min_rows;
   if (!pl.used) return pl;
   const int64_t rows = p.T * g;
@@ -95,6 +106,8 @@ Plan plan_rows(int dtype, const PagedAttn& p, bool with_keys) {
   if (part > p.n_seqs) part = p.n_seqs;
   pl.tiles = (int)((rows + part * (kRowsTile - 1)) / kRowsTile);
   pl.part_rows = (size_t)pl.tiles * p.hkv * kRowsTile;
+  // Two workgroups a CU (one: 110 us for ragged float32 chunks, two: 87, three or
+  // four: 102; bf16 chunks beside single tokens 745 with two, 748 to 802 with more).
   split(&pl, p, key_span(p, kRowsTile / g + 2), (int64_t)pl.tiles * p.hkv, 2 * kCus,
         dtype == 1 ? 256 : 128, 1 << 30);
   return pl;
@@ -123,7 +136,9 @@ template <typename T>
 hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipStream_t s) {
   const PagedAttn& p = a.p;
   // see TileLoader: rows looked up together, lane offsets of less than 32 rows in
-  // 32 bits
+  // 32 bits.  Pages of 16: a 4096-token prompt 108 us, by 8 rows 112, row by row 121;
+  // chunks beside single tokens 722, 737, 790.  Pages of 24: prompt 109 by 8 rows and 117
+  // row by row (float32 chunks 84 and 81).
   const bool near = p.kc_token < (1 << 24) && p.vc_token < (1 << 24);
   const int granule = !near ? 0 : p.page_size % 16 == 0 ? 16 : p.page_size % 8 == 0 ? 8 : 0;
   hipError_t e = hipSuccess;
@@ -140,7 +155,9 @@ hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipS
   }
   if (keys.used) {
     place(&a, keys, ws);
-
+    // Beside attn_rows most of the tiles that the host counts are not there, so the items
+    // are numbered on the device: chunks beside single tokens 713 us, with a workgroup for
+    // each 721; 16 float32 sequences 88 and 98; but 5 float32 chunks 84 and 80.
     e = launch_attn_keys<T>(a, granule, rows.used, s);
     if (e != hipSuccess) return e;
     if (keys.splits > 1) {

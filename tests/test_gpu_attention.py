@@ -386,6 +386,26 @@ def test_attention_splits_and_groups(q_lens, kv_lens, hq, hkv, D, page, dtype, c
     test_attention(q_lens, kv_lens, hq, hkv, D, page, dtype, causal, window, order)
 
 
+FEW_AND_MANY_ROWS = [
+    # rows around one and two tiles of few rows, with and without longer sequences beside
+    # them: 32, 33 .. 64 and 65 rows of a sequence
+    ([8, 9, 16, 17, 1], [300, 90, 700, 130, 2000], 8, 2, 128, 16, 0),
+    ([8, 9, 16, 1], [300, 90, 700, 2000], 8, 2, 128, 16, 0),
+    ([32, 33, 64, 65, 1, 0], [40, 900, 64, 65, 3, 9], 3, 3, 64, 24, 0),
+    ([16, 17, 33], [1500, 1400, 33], 4, 2, 80, 1, 70),
+    # a single token has more rows than one tile, or than two
+    ([1, 2, 30], [500, 40, 300], 48, 1, 64, 16, 0),
+    ([1, 1], [1200, 7], 48, 1, 128, 8, 0),
+    ([1, 5, 1], [900, 5, 0], 130, 2, 64, 16, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("q_lens,kv_lens,hq,hkv,D,page,window", FEW_AND_MANY_ROWS)
+def test_few_and_many_rows(q_lens, kv_lens, hq, hkv, D, page, window, dtype):
+    test_attention(q_lens, kv_lens, hq, hkv, D, page, dtype, True, window, "token")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n_seqs,long", [(70, 0), (150, 5), (300, 0), (65, 65)])
 def test_many_sequences(dtype, n_seqs, long):
