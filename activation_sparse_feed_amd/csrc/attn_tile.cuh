@@ -198,14 +198,16 @@ struct AttnTile {
 
   // Moves the running maximum to that of the scores (and scales l and o) where
   // some row's grows by more than a factor of 2^8: weights up to 2^8 keep their
-  // relative precision in any type, and most blocks then leave o alone.
+  // relative precision in any type, and most blocks then leave o alone.  A row
+  // without a maximum yet has l = 0, and in o nothing but infinite values that
+  // add_infinite put there: they stay (the factor exp2(-inf) = 0 would make NaN of them).
   __device__ __forceinline__ void raise(const f32x16_t& s, float c) {
     float mx = s[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
     const float mn = fmaxf(m, max_halves(mx));
     if (__any((mn - m) * c > 8.f)) {
-      const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * c);
+      const float f = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * c);
       l *= f;
 #pragma unroll
       for (int d = 0; d < kDt; ++d)

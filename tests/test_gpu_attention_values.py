@@ -1,0 +1,60 @@
+"""Infinities, NaN and extreme limits in paged_attn_fwd: results that follow from the
+definition without rounding, so they are compared exactly."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from test_gpu_attention import _attention_case, _run
+
+pytestmark = pytest.mark.gpu
+
+
+INFINITE = [
+    # q_len, kv_len, D, page, window, keys
+    # the first tiles of a prompt, which the first rows see in part
+    (100, 100, 64, 16, 0, (0, 1, 31, 40, 63, 64)),
+    (300, 300, 128, 16, 0, (0, 5, 130)),
+    (70, 70, 96, 24, 0, (0, 33)),
+    (90, 90, 256, 16, 0, (0, 33)),
+    # the start of a window
+    (100, 700, 64, 16, 60, (541, 545, 600)),
+    # split ranges, from the start and from inside a window
+    (100, 3000, 128, 16, 0, (0, 2900, 2950)),
+    (90, 2800, 64, 8, 700, (2011, 2040, 2700)),
+    # few rows
+    (4, 60, 64, 16, 0, (0, 56, 58)),
+    (4, 900, 128, 16, 100, (797, 798, 850)),
+    (3, 9000, 128, 8, 0, (0, 5000, 8997)),
+    (2, 9000, 64, 16, 5000, (3999, 4500, 8998)),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("q_len,kv_len,D,page,window,keys", INFINITE)
+def test_infinite_values_reach_the_rows_that_see_them(q_len, kv_len, D, page, window, keys, bad, dtype):
+    """An infinite element of a value is the result's for every row that sees it (a
+    positive weight times infinity), and everything else is as without it."""
+    c = _attention_case([q_len], [kv_len], 4, 2, D, page, dtype, seed=kv_len)
+    clean, clean_l = _run(c, window=window)
+    pos = torch.arange(kv_len - q_len, kv_len, device="cuda")
+    for j in keys:
+        at = c["v"][int(c["bt"][0, j // page]), j % page]
+        kept = at.clone()
+        at[:, 3::5] = bad
+        out, lse = _run(c, window=window)
+        at.copy_(kept)
+        seen = pos >= j
+        if window:
+            seen &= pos < j + window
+        assert seen.any()
+        want = clean.clone()
+        part = want[:, :, 3::5]
+        part[seen] = bad
+        assert torch.equal(torch.isnan(out), torch.isnan(want))
+        same = (out == want) | torch.isnan(want)
+        assert same.all(), (j, (~same).nonzero()[:4].tolist())
+        assert torch.equal(lse, clean_l)
