@@ -505,8 +505,7 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys(AttnArgs
         const float mk = ml[k][rr][0];
         const float f = mk == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mk - m);
         l += f * ml[k][rr][1];
-        if (mk != -INFINITY)
-          v += f * *(const f32x4_t*)(part(k, d / 32) + rr * 128 + (((d % 32 / 4) ^ (rr & 7)) << 4));
+        v += f * *(const f32x4_t*)(part(k, d / 32) + rr * 128 + (((d % 32 / 4) ^ (rr & 7)) << 4));
       }
       const int tk = a.group.div(r0 + rr), hd = hk * a.g + r0 + rr - tk * a.g;
       if (kw.n_split == 1) {
@@ -586,14 +585,15 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
     const float* o = a.part_o + slot * p.D + (d < p.D ? d : 0);
     // loads without conditions, so that they are in flight together: a split past the
-    // last one repeats it with a factor of 0
+    // last one reads it again and drops it.  A factor of 0 drops nothing: NaN times it
+    // stays NaN, as in a sum over all keys
 #pragma unroll 8
     for (int s0 = kShare == 4 ? wave * side : 0; s0 < n; s0 += side * kShare) {
       const int s = s0 + sub, sc = min(s, n - 1);
-      const float fc = __shfl(f, sc, kWave), fs = s < n ? fc : 0.f;
+      const float fs = __shfl(f, sc, kWave);
       const f32x4_t x = *(const f32x4_t*)(o + (size_t)sc * a.part_rows * p.D);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += fs == 0.f ? 0.f : fs * x[i];
+      for (int i = 0; i < 4; ++i) v[i] += s < n ? fs * x[i] : 0.f;
     }
     for (int k = width; k < kWave; k <<= 1)
 #pragma unroll

@@ -58,3 +58,22 @@ def test_infinite_values_reach_the_rows_that_see_them(q_len, kv_len, D, page, wi
         same = (out == want) | torch.isnan(want)
         assert same.all(), (j, (~same).nonzero()[:4].tolist())
         assert torch.equal(lse, clean_l)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("q_len,kv_len", [(1, 300), (1, 9001), (100, 200), (100, 3000)])
+def test_nan_of_vanishing_weight_is_not_lost(q_len, kv_len, dtype):
+    """The first half of the keys has scores of -800, whose weights are 0 in float32; a
+    NaN among their values is the result's all the same, whether or not these keys are
+    a split of their own."""
+    c = _attention_case([q_len], [kv_len], 4, 2, 64, 16, dtype, seed=kv_len)
+    c["q"][:] = 1.0
+    for j in range(kv_len // 2):
+        c["k"][int(c["bt"][0, j // 16]), j % 16] = -100.0   # scores of -100 * 64 / 8
+    clean, clean_l = _run(c)
+    c["v"][int(c["bt"][0, 0]), 10, :, 3::5] = math.nan
+    out, lse = _run(c)
+    bad = torch.zeros(64, dtype=torch.bool, device="cuda")
+    bad[3::5] = True
+    assert torch.isnan(out[:, :, bad]).all()
+    assert torch.equal(out[:, :, ~bad], clean[:, :, ~bad]) and torch.equal(lse, clean_l)
