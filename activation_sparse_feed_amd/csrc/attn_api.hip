@@ -99,7 +99,10 @@ PagedAttn attn_params(const sffn_paged_batch* b) {
   p.T = b->T, p.n_seqs = b->n_seqs, p.hq = b->n_q_heads, p.hkv = b->n_kv_heads, p.D = b->head_dim;
   p.page_size = b->page_size, p.n_pages = b->n_pages, p.max_pages = b->max_pages;
   p.max_q = b->max_q < b->T ? b->max_q : b->T;
-  p.max_kv = b->max_kv, p.causal = b->causal, p.window = b->window, p.scale = b->scale;
+  p.max_kv = b->max_kv, p.causal = b->causal, p.scale = b->scale;
+  // a window as long as every sequence hides nothing; a shorter one keeps position
+  // minus window within 32 bits, also at the negative positions of rows before the keys
+  p.window = b->window < b->max_kv ? b->window : 0;
   return p;
 }
 

@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_attention import _attention_case, _run
+from test_gpu_attention import _attention_case, _check_attention, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,17 @@ def test_nan_of_vanishing_weight_is_not_lost(q_len, kv_len, dtype):
     bad[3::5] = True
     assert torch.isnan(out[:, :, bad]).all()
     assert torch.equal(out[:, :, ~bad], clean[:, :, ~bad]) and torch.equal(lse, clean_l)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 40, 1 << 30, 1500])
+@pytest.mark.parametrize("q_lens,kv_lens", [([5, 1, 40], [2, 900, 33]), ([150, 3], [20, 1500])])
+def test_windows_that_hide_nothing(q_lens, kv_lens, window, causal, dtype):
+    """A window of at least every sequence's length is none, up to the largest number, also
+    where a sequence has more rows than keys (its first positions are negative)."""
+    c = _attention_case(q_lens, kv_lens, 4, 2, 64, 16, dtype, seed=31)
+    out, lse = _run(c, causal, window)
+    _check_attention(c, out, lse, causal, window)
+    free, free_l = _run(c, causal, 0)
+    assert torch.equal(out, free) and torch.equal(lse, free_l)
