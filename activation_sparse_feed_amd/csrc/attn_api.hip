@@ -75,6 +75,18 @@ int32_t check_cache(const void* c, int64_t n_pages, int64_t sp, int64_t page_siz
                       check_rows(c, n_pages, sp, heads, sh, D, dtype, true)});
 }
 
+PagedAttn attn_params(const sffn_paged_batch* b) {
+  PagedAttn p = {};
+  p.T = b->T, p.n_seqs = b->n_seqs, p.hq = b->n_q_heads, p.hkv = b->n_kv_heads, p.D = b->head_dim;
+  p.page_size = b->page_size, p.n_pages = b->n_pages, p.max_pages = b->max_pages;
+  p.max_q = b->max_q < b->T ? b->max_q : b->T;
+  p.max_kv = b->max_kv, p.causal = b->causal, p.scale = b->scale;
+  // a window as long as every sequence hides nothing; a shorter one keeps position
+  // minus window within 32 bits, also at the negative positions of rows before the keys
+  p.window = b->window < b->max_kv ? b->window : 0;
+  return p;
+}
+
 int32_t check_batch(const sffn_paged_batch* b) {
   if (b == nullptr) return SFFN_ERR_ARG;
   if (b->T < 0 || b->n_seqs < 0 || b->n_q_heads <= 0 || b->n_kv_heads <= 0 || b->head_dim <= 0 ||
@@ -91,19 +103,7 @@ int32_t check_batch(const sffn_paged_batch* b) {
   if ((int64_t)b->T * b->n_q_heads > (1 << 30) || b->max_kv > (1 << 30) || b->n_seqs > (1 << 20) ||
       b->n_q_heads > 4096)
     return SFFN_ERR_UNSUPPORTED;
-  return SFFN_OK;
-}
-
-PagedAttn attn_params(const sffn_paged_batch* b) {
-  PagedAttn p = {};
-  p.T = b->T, p.n_seqs = b->n_seqs, p.hq = b->n_q_heads, p.hkv = b->n_kv_heads, p.D = b->head_dim;
-  p.page_size = b->page_size, p.n_pages = b->n_pages, p.max_pages = b->max_pages;
-  p.max_q = b->max_q < b->T ? b->max_q : b->T;
-  p.max_kv = b->max_kv, p.causal = b->causal, p.scale = b->scale;
-  // a window as long as every sequence hides nothing; a shorter one keeps position
-  // minus window within 32 bits, also at the negative positions of rows before the keys
-  p.window = b->window < b->max_kv ? b->window : 0;
-  return p;
+  return paged_attn_fits(b->dtype, attn_params(b)) ? SFFN_OK : SFFN_ERR_UNSUPPORTED;
 }
 
 }  // namespace

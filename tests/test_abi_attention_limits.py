@@ -1,0 +1,36 @@
+"""Sizes at and beyond what the attention side's launches take, on the host: refused
+before anything is launched, and accepted up to the limit.  An accepted size shows as the
+complaint about a missing buffer that is looked at next, so nothing is launched here."""
+from __future__ import annotations
+
+import pytest
+
+from test_abi_attention import ARG, UNSUPPORTED, attn, batch, sffn  # noqa: F401
+
+NONE = (None, 512, 64)
+
+
+@pytest.mark.parametrize("kw,status", [
+    # single tokens, head_dim 128: workgroups of four waves, 2^32 threads are too many
+    (dict(n_seqs=1 << 20, n_q_heads=16, n_kv_heads=16, head_dim=128), UNSUPPORTED),
+    (dict(n_seqs=(1 << 20) - 1, n_q_heads=16, n_kv_heads=16, head_dim=128), ARG),
+    # head_dim 64: eight waves
+    (dict(n_seqs=1 << 20, n_q_heads=8, n_kv_heads=8), UNSUPPORTED),
+    (dict(n_seqs=1 << 20, n_q_heads=7, n_kv_heads=7), ARG),
+    # products of tiles and key heads beyond 32 bits
+    (dict(n_seqs=1 << 20, n_q_heads=2048, n_kv_heads=2048), UNSUPPORTED),
+    (dict(n_seqs=1 << 20, n_q_heads=4096, n_kv_heads=4096), UNSUPPORTED),
+    (dict(n_seqs=1 << 20, n_q_heads=4096, n_kv_heads=4096, max_kv=0), UNSUPPORTED),
+    # chunks among many sequences: tiles of many rows, and items numbered on the device
+    (dict(T=1 << 18, max_q=1000, n_seqs=1 << 18, n_q_heads=4096, n_kv_heads=4096), UNSUPPORTED),
+    (dict(T=5000, max_q=1000, n_seqs=1 << 20, n_q_heads=4096, n_kv_heads=4096, max_kv=64), UNSUPPORTED),
+    (dict(T=5000, max_q=1000, n_seqs=1 << 12, n_q_heads=64, n_kv_heads=8), ARG),
+    # nothing but chunks: T = n_seqs * max_q
+    (dict(T=1 << 18, max_q=1 << 6, n_seqs=1 << 12, n_q_heads=4096, n_kv_heads=1), ARG),
+    (dict(T=1 << 18, max_q=65, n_seqs=1 << 18, n_q_heads=4096, n_kv_heads=4096, max_kv=0), UNSUPPORTED),
+])
+def test_grids_of_the_attention(sffn, kw, status):  # noqa: F811
+    b = batch(sffn, **kw)
+    assert attn(sffn, b, q=NONE) == status
+    if status != ARG:
+        assert sffn._lib.paged_attn_workspace_bytes(b) == 0
