@@ -40,8 +40,16 @@ int32_t check_heads(const sffn_heads* h) {
   if (h->dtype != SFFN_F32 && h->dtype != SFFN_BF16) return SFFN_ERR_ARG;
   if (h->rot_dim > 0 && h->max_pos == 0) return SFFN_ERR_ARG;
   if (h->head_dim % 8 != 0 || h->head_dim > 256 || h->rot_dim % 4 != 0) return SFFN_ERR_UNSUPPORTED;
-  if (h->n_q_heads > 4096 || h->n_kv_heads > 4096) return SFFN_ERR_UNSUPPORTED;
+  // token numbers, and one step of the backward's grid past them, are 32-bit
+  if (h->n_q_heads > 4096 || h->n_kv_heads > 4096 || h->T > (1 << 30)) return SFFN_ERR_UNSUPPORTED;
   return SFFN_OK;
+}
+
+// The forward and the append have 64 threads a token in one grid, which has less than
+// 2^32 of them.
+int32_t check_heads_fwd(const sffn_heads* h) {
+  const int32_t st = check_heads(h);
+  return st == SFFN_OK && h->T > (1 << 26) - 4 ? SFFN_ERR_UNSUPPORTED : st;
 }
 
 int32_t check_rotation(const sffn_heads* h, const void* q_weight, const void* k_weight,
@@ -115,7 +123,7 @@ int32_t qk_norm_rope(const sffn_heads* heads, const void* q, int64_t q_token, in
                      const void* k_weight, const float* rot_table, const int32_t* positions,
                      void* q_out, int64_t qo_token, int64_t qo_head, void* k_out,
                      int64_t ko_token, int64_t ko_head, void* stream) {
-  int32_t st = check_heads(heads);
+  int32_t st = check_heads_fwd(heads);
   if (st != SFFN_OK) return st;
   const sffn_heads& h = *heads;
   if (h.T == 0 || h.n_q_heads + h.n_kv_heads == 0) return SFFN_OK;
@@ -196,7 +204,7 @@ int32_t paged_kv_append(const sffn_heads* heads, const void* q, int64_t q_token,
                         void* k_cache, int64_t kc_page, int64_t kc_token, int64_t kc_head,
                         void* v_cache, int64_t vc_page, int64_t vc_token, int64_t vc_head,
                         int32_t n_pages, int32_t page_size, void* stream) {
-  int32_t st = check_heads(heads);
+  int32_t st = check_heads_fwd(heads);
   if (st != SFFN_OK) return st;
   const sffn_heads& h = *heads;
   if (h.n_kv_heads == 0 || n_pages < 0 || page_size <= 0) return SFFN_ERR_ARG;

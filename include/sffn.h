@@ -457,7 +457,8 @@ int32_t sffn_probe_bf16_round(const float* in, uint16_t* out, size_t n, void* st
 
 /* Heads of q and k: their norm and rotation. */
 typedef struct {
-  int32_t T;            /* tokens; 0: nothing to do */
+  int32_t T;            /* tokens; 0: nothing to do; at most 2^26 - 4, in
+                           qk_norm_rope_bwd 2^30 */
   int32_t n_q_heads;    /* heads of q, may be 0 (then q, q_out, ... are NULL) */
   int32_t n_kv_heads;   /* heads of k (and v), may be 0 except in paged_kv_append */
   int32_t head_dim;     /* a multiple of 8, 8 .. 256 */
@@ -529,7 +530,10 @@ int32_t paged_kv_append(const sffn_heads* heads, const void* q, int64_t q_token,
 /* A batch of sequences over a paged cache. */
 typedef struct {
   int32_t T;          /* rows of q (new tokens of all sequences) */
-  int32_t n_seqs;
+  int32_t n_seqs;     /* at most 2^20; times n_kv_heads below 2^23 is always taken where
+                         no sequence has more than 32 rows (new tokens times the query
+                         heads of a key head), more is refused as unsupported where its
+                         grid has 2^32 threads */
   int32_t n_q_heads;  /* a multiple of n_kv_heads */
   int32_t n_kv_heads;
   int32_t head_dim;   /* a multiple of 8, 8 .. 256 */

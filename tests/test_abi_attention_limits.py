@@ -5,7 +5,8 @@ from __future__ import annotations
 
 import pytest
 
-from test_abi_attention import ARG, UNSUPPORTED, attn, batch, sffn  # noqa: F401
+from test_abi_attention import (ARG, UNSUPPORTED, append, attn, batch, heads, norm_rope,  # noqa: F401
+                                norm_rope_bwd, sffn)
 
 NONE = (None, 512, 64)
 
@@ -34,3 +35,16 @@ def test_grids_of_the_attention(sffn, kw, status):  # noqa: F811
     assert attn(sffn, b, q=NONE) == status
     if status != ARG:
         assert sffn._lib.paged_attn_workspace_bytes(b) == 0
+
+
+def test_grids_of_the_heads(sffn):  # noqa: F811
+    """64 threads a token in the forward and the append; the backward walks over tokens."""
+    for T, status in (((1 << 26) - 4, ARG), ((1 << 26) - 3, UNSUPPORTED), (1 << 26, UNSUPPORTED),
+                      ((1 << 31) - 1, UNSUPPORTED)):
+        h = heads(sffn, T=T)
+        assert norm_rope(sffn, h, q=NONE) == status and append(sffn, h, q=NONE) == status
+    for T, status in ((1 << 26, ARG), (1 << 30, ARG), ((1 << 30) + 1, UNSUPPORTED),
+                      ((1 << 31) - 1, UNSUPPORTED)):
+        h = heads(sffn, T=T)
+        assert norm_rope_bwd(sffn, h, q=NONE) == status
+        assert (sffn._lib.qk_norm_rope_bwd_workspace_bytes(h) > 0) == (status == ARG)
