@@ -208,6 +208,8 @@ int32_t paged_kv_append(const sffn_heads* heads, const void* q, int64_t q_token,
   if (st != SFFN_OK) return st;
   const sffn_heads& h = *heads;
   if (h.n_kv_heads == 0 || n_pages < 0 || page_size <= 0) return SFFN_ERR_ARG;
+  // a slot has 32 bits: tokens past it would be taken for padding, or wrap onto others
+  if ((int64_t)n_pages * page_size > (1ll << 31)) return SFFN_ERR_UNSUPPORTED;
   if (h.T == 0) return SFFN_OK;
   st = check_rotation(heads, q_weight, k_weight, rot_table, positions);
   if (st == SFFN_OK && h.n_q_heads > 0)

@@ -515,7 +515,8 @@ size_t qk_norm_rope_bwd_workspace_bytes(const sffn_heads* heads);
  * q normalised and rotated into q_out, k normalised and rotated into k_cache, v
  * copied into v_cache.  slots: int32 [T], the cache row of each token:
  * page * page_size + offset in the page; a slot outside the cache (-1 for a
- * padding token) is not stored.  Two tokens with one slot: which is kept is
+ * padding token) is not stored, and a cache of more than 2^31 rows, which slots
+ * cannot name, is unsupported.  Two tokens with one slot: which is kept is
  * not specified.  With n_q_heads == 0 only the cache is written.
  */
 int32_t paged_kv_append(const sffn_heads* heads, const void* q, int64_t q_token, int64_t q_head,

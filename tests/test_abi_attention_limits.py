@@ -48,3 +48,10 @@ def test_grids_of_the_heads(sffn):  # noqa: F811
         h = heads(sffn, T=T)
         assert norm_rope_bwd(sffn, h, q=NONE) == status
         assert (sffn._lib.qk_norm_rope_bwd_workspace_bytes(h) > 0) == (status == ARG)
+
+
+def test_rows_of_a_cache_fit_a_slot(sffn):  # noqa: F811
+    h = heads(sffn)
+    assert append(sffn, h, q=NONE, n_pages=1 << 27, page=16) == ARG
+    assert append(sffn, h, q=NONE, n_pages=(1 << 27) + 1, page=16) == UNSUPPORTED
+    assert append(sffn, h, q=NONE, n_pages=(1 << 31) - 1, page=(1 << 31) - 1) == UNSUPPORTED
