@@ -445,6 +445,12 @@ def _array(name: str, t, n: int, dtype):
     return t.data_ptr()
 
 
+def _columns(name: str, t, cols: int):
+    """The kernels step over rows of `cols` elements: a table with others would be misread."""
+    if t is not None and t.dim() == 2 and t.shape[1] != cols:
+        raise ValueError(f"{name} must have {cols} columns, not {t.shape[1]}")
+
+
 def _rotation(h: Heads, q_weight, k_weight, table, positions, dt):
     if h.rot_dim and table is not None and table.dim() == 2 and table.shape[1] != h.rot_dim:
         raise ValueError(f"the rotation table must be [max_pos, {h.rot_dim}]")
@@ -532,6 +538,8 @@ def paged_attn_fwd(batch: PagedBatch, q, k_cache, v_cache, q_start, kv_len, bloc
     its kv_len[s] cached keys, found through block_table [n_seqs, max_pages]."""
     T, D, dt = batch.T, batch.head_dim, _TORCH_DTYPE[batch.dtype]
     nq, nk, ns = batch.n_q_heads, batch.n_kv_heads, batch.n_seqs
+    _columns("block_table", block_table, batch.max_pages)
+    _columns("lse", lse, nq)
     ws, ws_n = (None, 0) if workspace is None else \
         (_ptr(workspace), workspace.numel() * workspace.element_size())
     _check("paged_attn_fwd", _lib.paged_attn_fwd(
