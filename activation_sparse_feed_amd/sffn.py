@@ -445,6 +445,13 @@ def _array(name: str, t, n: int, dtype):
     return t.data_ptr()
 
 
+def _weight(name: str, t, dim: int, dtype):
+    """Pointer of a norm's weights or their gradients: one row for all heads."""
+    if t is not None and t.numel() != dim:
+        raise ValueError(f"{name} must have {dim} elements, not {t.numel()}")
+    return _array(name, t, dim, dtype)
+
+
 def _columns(name: str, t, cols: int):
     """The kernels step over rows of `cols` elements: a table with others would be misread."""
     if t is not None and t.dim() == 2 and t.shape[1] != cols:
@@ -454,8 +461,8 @@ def _columns(name: str, t, cols: int):
 def _rotation(h: Heads, q_weight, k_weight, table, positions, dt):
     if h.rot_dim and table is not None and table.dim() == 2 and table.shape[1] != h.rot_dim:
         raise ValueError(f"the rotation table must be [max_pos, {h.rot_dim}]")
-    return (_array("q_weight", q_weight, h.head_dim, dt),
-            _array("k_weight", k_weight, h.head_dim, dt),
+    return (_weight("q_weight", q_weight, h.head_dim, dt),
+            _weight("k_weight", k_weight, h.head_dim, dt),
             _array("the rotation table", table, h.max_pos * h.rot_dim, torch.float32),
             _array("positions", positions, h.T, torch.int32))
 
@@ -499,8 +506,8 @@ def qk_norm_rope_bwd(heads: Heads, q, k, q_weight, k_weight, table, positions, g
         *_rotation(heads, q_weight, k_weight, table, positions, dt),
         *_rows("gq_out", gq_out, T, nq, D, dt), *_rows("gk_out", gk_out, T, nk, D, dt),
         *_rows("gq", gq, T, nq, D, dt), *_rows("gk", gk, T, nk, D, dt),
-        _array("gq_weight", gq_weight, D, torch.float32),
-        _array("gk_weight", gk_weight, D, torch.float32), ws, ws_n, _stream_ptr(stream)))
+        _weight("gq_weight", gq_weight, D, torch.float32),
+        _weight("gk_weight", gk_weight, D, torch.float32), ws, ws_n, _stream_ptr(stream)))
 
 
 def paged_kv_append(heads: Heads, q, k, v, q_weight, k_weight, table, positions, slots, q_out,

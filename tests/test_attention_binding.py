@@ -55,3 +55,38 @@ def test_columns_of_the_tables(sffn):  # noqa: F811
         attention(sffn, block_table=gpu(1, 5, dtype=torch.int32))
     with pytest.raises(ValueError, match="lse must have 4 columns"):
         attention(sffn, lse=gpu(4, 8, dtype=torch.float32))
+
+
+def rotated(sffn, name="qk_norm_rope", **kw):  # noqa: F811
+    """The heads of q and k (forward, backward or append), 8 tokens, 4 heads on 2 of 64."""
+    h = sffn.make_heads(8, 4, 2, 64, torch.bfloat16, norm=True, eps=float("nan"))
+    q, k, w = gpu(8, 4, 64), gpu(8, 2, 64), gpu(64)
+    a = dict(q_weight=w, k_weight=w)
+    a.update(kw)
+    head = [h, q, k] + ([k] if name == "paged_kv_append" else [])
+    head += [a.pop("q_weight"), a.pop("k_weight"), None, None]
+    if name == "qk_norm_rope":
+        sffn.qk_norm_rope(*head, q, k, stream=_NoStream)
+    elif name == "paged_kv_append":
+        sffn.paged_kv_append(*head, gpu(8, dtype=torch.int32), q, gpu(4, 16, 2, 64),
+                             gpu(4, 16, 2, 64), stream=_NoStream)
+    else:
+        g = gpu(64, dtype=torch.float32)
+        sffn.qk_norm_rope_bwd(*head, q, k, q, k, a.get("gq_weight", g), a.get("gk_weight", g),
+                              gpu(1 << 16, dtype=torch.uint8), stream=_NoStream)
+
+
+def test_norm_weights_are_one_row(sffn):  # noqa: F811
+    """Weights of every head would be taken for those of the first."""
+    for name in ("qk_norm_rope", "paged_kv_append", "qk_norm_rope_bwd"):
+        accepted(sffn, rotated, name=name)
+        accepted(sffn, rotated, name=name, q_weight=gpu(1, 64), k_weight=None)
+        for bad in (gpu(4, 64), gpu(128), gpu(60)):
+            with pytest.raises(ValueError, match="q_weight must have 64 elements"):
+                rotated(sffn, name=name, q_weight=bad)
+            with pytest.raises(ValueError, match="k_weight must have 64 elements"):
+                rotated(sffn, name=name, k_weight=bad)
+    with pytest.raises(ValueError, match="gq_weight must have 64 elements"):
+        rotated(sffn, "qk_norm_rope_bwd", gq_weight=gpu(4, 64, dtype=torch.float32))
+    with pytest.raises(ValueError, match="gk_weight must have 64 elements"):
+        rotated(sffn, "qk_norm_rope_bwd", gk_weight=gpu(2, 64, dtype=torch.float32))
