@@ -467,12 +467,17 @@ def _rotation(h: Heads, q_weight, k_weight, table, positions, dt):
             _array("positions", positions, h.T, torch.int32))
 
 
-def _stream_ptr(stream) -> int:
+def _stream_ptr(stream, t) -> int:
+    """The stream given, or the current one of the current device, on which a call's
+    tensors (t: one of them) must lie: its kernels would run beside their memory."""
     if stream is not None:
         return stream.cuda_stream
     # torch.cuda.current_stream().cuda_stream without building a Stream object,
     # which alone costs 2.5 us of the host's time for a small step
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    device = torch._C._cuda_getDevice()
+    if t is not None and t.get_device() != device:
+        raise ValueError(f"tensors are on GPU {t.get_device()}, the current device is {device}")
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def qk_norm_rope(heads: Heads, q, k, q_weight, k_weight, table, positions, q_out, k_out,
@@ -484,7 +489,7 @@ def qk_norm_rope(heads: Heads, q, k, q_weight, k_weight, table, positions, q_out
         heads, *_rows("q", q, T, nq, D, dt), *_rows("k", k, T, nk, D, dt),
         *_rotation(heads, q_weight, k_weight, table, positions, dt),
         *_rows("q_out", q_out, T, nq, D, dt), *_rows("k_out", k_out, T, nk, D, dt),
-        _stream_ptr(stream)))
+        _stream_ptr(stream, q if nq else k)))
 
 
 def alloc_heads_workspace(heads: Heads, device=None) -> torch.Tensor:
@@ -507,7 +512,8 @@ def qk_norm_rope_bwd(heads: Heads, q, k, q_weight, k_weight, table, positions, g
         *_rows("gq_out", gq_out, T, nq, D, dt), *_rows("gk_out", gk_out, T, nk, D, dt),
         *_rows("gq", gq, T, nq, D, dt), *_rows("gk", gk, T, nk, D, dt),
         _weight("gq_weight", gq_weight, D, torch.float32),
-        _weight("gk_weight", gk_weight, D, torch.float32), ws, ws_n, _stream_ptr(stream)))
+        _weight("gk_weight", gk_weight, D, torch.float32), ws, ws_n,
+        _stream_ptr(stream, gq_out if nq else gk_out)))
 
 
 def paged_kv_append(heads: Heads, q, k, v, q_weight, k_weight, table, positions, slots, q_out,
@@ -525,7 +531,7 @@ def paged_kv_append(heads: Heads, q, k, v, q_weight, k_weight, table, positions,
         _array("slots", slots, T, torch.int32), *_rows("q_out", q_out, T, nq, D, dt),
         *_cache("k_cache", k_cache, n_pages, page_size, nk, D, dt),
         *_cache("v_cache", v_cache, n_pages, page_size, nk, D, dt), n_pages, page_size,
-        _stream_ptr(stream)))
+        _stream_ptr(stream, k_cache)))
 
 
 def paged_attn_workspace_bytes(batch: PagedBatch) -> int:
@@ -556,7 +562,7 @@ def paged_attn_fwd(batch: PagedBatch, q, k_cache, v_cache, q_start, kv_len, bloc
         _array("q_start", q_start, ns + 1, torch.int32), _array("kv_len", kv_len, ns, torch.int32),
         _array("block_table", block_table, ns * batch.max_pages, torch.int32),
         *_rows("out", out, T, nq, D, dt), _array("lse", lse, T * nq, torch.float32), ws, ws_n,
-        _stream_ptr(stream)))
+        _stream_ptr(stream, out)))
 
 
 def paged_slots(block_table, seq, positions, page_size: int) -> torch.Tensor:

@@ -90,3 +90,19 @@ def test_norm_weights_are_one_row(sffn):  # noqa: F811
         rotated(sffn, "qk_norm_rope_bwd", gq_weight=gpu(4, 64, dtype=torch.float32))
     with pytest.raises(ValueError, match="gk_weight must have 64 elements"):
         rotated(sffn, "qk_norm_rope_bwd", gk_weight=gpu(2, 64, dtype=torch.float32))
+
+
+def test_tensors_of_another_device(sffn, monkeypatch):  # noqa: F811
+    """Without a stream the current device's is used: tensors of another are refused."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+    here = 0
+    monkeypatch.setattr(OnGpu, "get_device", lambda self: here, raising=False)
+    for call in (attention, *(lambda m, n=n: rotated(m, n) for n in
+                              ("qk_norm_rope", "paged_kv_append", "qk_norm_rope_bwd"))):
+        monkeypatch.setitem(globals(), "_NoStream", None)   # the current stream
+        here = 0
+        with pytest.raises(ValueError, match="on GPU 0, the current device is 1"):
+            call(sffn)
+        here = 1
+        accepted(sffn, call)
