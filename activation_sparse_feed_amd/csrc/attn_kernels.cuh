@@ -263,7 +263,9 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
 
   Tile tile;
   tile.init();
-  if (p.D != DP) {  // chunks that are read, but that no load writes
+  // chunks that no load writes, but that are read: up to DP by the products, up to the
+  // end of the LDS row by the search for infinite values
+  if (p.D != Tile::kRowElems) {
     for (int i = threadIdx.x * 16; i < Tile::kTileBytes; i += NW * 64 * 16)
       *(u32x4_t*)(k0 + i) = *(u32x4_t*)(k1 + i) = *(u32x4_t*)(v0 + i) = *(u32x4_t*)(v1 + i) =
           u32x4_t{0u, 0u, 0u, 0u};
@@ -374,8 +376,8 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys(AttnArgs
   const PagedAttn& p = a.p;
   const int wave = uniform((int)threadIdx.x / kWave), lane = lane_id(), half = lane >> 5;
   uint8_t *const k = k_lds[wave], *const v = v_lds[wave];
-  auto clear = [&]() __attribute__((always_inline)) {  // chunks that are read, but that no load writes
-    if (p.D == DP) return;
+  auto clear = [&]() __attribute__((always_inline)) {  // as in attn_rows
+    if (p.D == Tile::kRowElems) return;
     for (int i = lane * 16; i < Tile::kTileBytes; i += kWave * 16)
       *(u32x4_t*)(k + i) = *(u32x4_t*)(v + i) = u32x4_t{0u, 0u, 0u, 0u};
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): written

@@ -91,3 +91,45 @@ def test_windows_that_hide_nothing(q_lens, kv_lens, window, causal, dtype):
     _check_attention(c, out, lse, causal, window)
     free, free_l = _run(c, causal, 0)
     assert torch.equal(out, free) and torch.equal(lse, free_l)
+
+
+@pytest.mark.parametrize("D", [96, 192])
+@pytest.mark.parametrize("q_lens,kv_lens,window", [([2000], [2000], 200), ([1, 3, 40, 2], [900, 300, 500, 2000], 0)])
+def test_widths_between_the_lds_rows(D, q_lens, kv_lens, window):
+    """Rows of 96 and 192 elements leave a part of their LDS rows unused."""
+    c = _attention_case(q_lens, kv_lens, 4, 2, D, 16, "bf16", seed=D)
+    out, lse = _run(c, window=window)
+    _check_attention(c, out, lse, window=window)
+
+
+def test_time_does_not_depend_on_what_lds_held():
+    """A prompt of width 96 in a window after a call that leaves infinities everywhere in LDS
+    takes as long as after one that leaves finite numbers: the unused part of an LDS row is not
+    searched for them.  Medians of 15, and a factor of two for noise (it was five)."""
+    from activation_sparse_feed_amd import sffn
+
+    def call(D, n, window, value=None):
+        c = _attention_case([n], [n], 16, 4, D, 16, "bf16", seed=D)
+        if value is not None:
+            c["k"].fill_(value)
+            c["v"].fill_(value)
+        b = sffn.make_paged_batch(n, 1, 16, 4, D, torch.bfloat16, 16, c["n_pages"], c["bt"].shape[1],
+                                  n, n, window=window)
+        dev = [torch.from_numpy(c[x]).cuda() for x in ("qs", "kv", "bt")]
+        out, ws = torch.empty((n, 16, D), dtype=torch.bfloat16, device="cuda"), sffn.alloc_paged_workspace(b)
+        return lambda: sffn.paged_attn_fwd(b, c["q"], c["k"], c["v"], *dev, out, ws)
+
+    timed = call(96, 4096, 300)
+    medians = []
+    for value in (1.0, math.inf):
+        before, times = call(256, 1024, 0, value), []
+        for _ in range(15):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            before()
+            start.record()
+            timed()
+            end.record()
+            torch.cuda.synchronize()
+            times.append(start.elapsed_time(end))
+        medians.append(sorted(times)[7])
+    assert medians[1] < 2 * medians[0], medians
