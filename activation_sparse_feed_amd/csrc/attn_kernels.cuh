@@ -516,8 +516,7 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys(AttnArgs
                   v[1] * inv, v[2] * inv, v[3] * inv);
         if (d == 0 && p.lse != nullptr) p.lse[(int64_t)(w.q0 + tk) * p.hq + hd] = finish_lse(m, l);
       } else {
-        const size_t slot = kw.split * a.part_rows +
-                            ((size_t)(w.seq * a.tiles_per_seq + w.tile) * p.hkv + hk) * 32 + rr;
+        const size_t slot = kw.split * a.part_rows + ((size_t)w.seq * p.hkv + hk) * a.slot_rows + r0 + rr;
         *(f32x4_t*)(a.part_o + slot * p.D + d) = v;
         if (d == 0) {
           a.part_ml[2 * slot] = m;
@@ -572,7 +571,8 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   const int side = kWave / width, sub = lane / width, d = (lane & (width - 1)) * 4;
   const int first = r0 + (kShare == 4 ? (int)blockIdx.y : (int)blockIdx.y * 4 + wave);
   for (int r = first; r <= r1; r += (int)gridDim.y * (4 / kShare)) {
-    const size_t slot = ((size_t)t * p.hkv + hk) * TM + (r - r0);
+    const size_t slot = TM == 32 ? ((size_t)w.seq * p.hkv + hk) * a.slot_rows + r
+                                 : ((size_t)t * p.hkv + hk) * TM + (r - r0);
     float ms = -INFINITY, ls = 0.f;
     if (lane < n) {
       const size_t at = lane * a.part_rows + slot;

@@ -64,6 +64,7 @@ struct AttnArgs {
   int min_rows;          // attn_rows takes sequences with more rows than this
   int max_rows;          // attn_keys takes sequences with at most so many
   int tiles_per_seq;     // attn_keys
+  int slot_rows;         // attn_keys: slots of a sequence and key head, for all rows it can have
   int splits;            // (bound of) splits of a key range
   int n_tiles;           // (bound of) row tiles of one key head
   float* part_o;         // [split][slot][D] outputs before the division, for split rows

@@ -16,13 +16,18 @@ namespace {
 constexpr int kRowsTile = 128;  // rows of an attn_rows workgroup
 constexpr int kKeysTile = 32;   // rows of an attn_keys workgroup
 constexpr int kMaxSplits = 64;  // lanes of the join
+// Partial results of one launch: max_kv is often the model's limit and not the batch's
+// longest sequence, and 1024 single tokens (8 key heads of 4 rows, width 128) would have
+// 1.1 GB of them in 64 splits.  They get 15 splits here, with which a sequence
+// of 131072 keys among short ones still has 120 workgroups.
+constexpr int64_t kMaxPartBytes = 256ll << 20;
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // What one launch takes: row tiles, splits, workspace.
 struct Plan {
   bool used;
-  int tiles, tiles_per_seq, min_rows, max_rows, chunk, splits;
+  int tiles, tiles_per_seq, min_rows, max_rows, slot_rows, chunk, splits;
   size_t part_rows, bytes;
 };
 
@@ -45,11 +50,15 @@ int64_t key_span(const PagedAttn& p, int64_t tokens) {
 }
 
 // Splits of a key range of at most `span` keys for `groups` workgroups: enough to
-// put `want` workgroups on the GPU, chunks of least .. most keys.
+// put `want` workgroups on the GPU, chunks of least .. most keys, and at most kMaxPartBytes
+// of partial results.
 void split(Plan* pl, const PagedAttn& p, int64_t span, int64_t groups, int64_t want, int least, int most) {
   int64_t n = groups > 0 ? (want + groups - 1) / groups : 1;
   // a range that does not start at a multiple of the chunk touches one more
-  const int64_t most_splits = p.window > 0 ? kMaxSplits - 1 : kMaxSplits;
+  const int64_t slot = (int64_t)(pl->part_rows * (p.D * 4 + 8)), fit = slot > 0 ? kMaxPartBytes / slot : kMaxSplits;
+  int64_t most_splits = fit < kMaxSplits ? fit : kMaxSplits;
+  if (p.window > 0) --most_splits;
+  if (most_splits < 1) most_splits = 1;
   int64_t chunk = (span + n - 1) / n;
   if (chunk > most) chunk = most;
   if (chunk < least) chunk = least;
@@ -78,7 +87,8 @@ Plan plan_keys(int dtype, const PagedAttn& p) {
   pl.max_rows = limit;
   pl.tiles_per_seq = (int)(((rows < limit ? rows : limit) + kKeysTile - 1) / kKeysTile);
   pl.tiles = p.n_seqs * pl.tiles_per_seq;
-  pl.part_rows = (size_t)pl.tiles * p.hkv * kKeysTile;
+  pl.slot_rows = (int)(rows < limit ? rows : limit);
+  pl.part_rows = (size_t)p.n_seqs * p.hkv * pl.slot_rows;
   // A wave takes 1 to 2 us for 32 keys (3 us in float32, whose products are 16 times
   // slower), the join and its launch 6 us: ranges of up to 5 (2) steps a wave
   // are not split.  Longer ones into chunks of 2 (1) to 6 (1) steps: 6 even out
@@ -118,6 +128,7 @@ void place(AttnArgs* a, const Plan& pl, void* ws) {
   a->min_rows = pl.min_rows;
   a->max_rows = pl.max_rows;
   a->tiles_per_seq = pl.tiles_per_seq;
+  a->slot_rows = pl.slot_rows;
   a->splits = pl.splits;
   a->n_tiles = pl.tiles;
   a->part_rows = pl.part_rows;

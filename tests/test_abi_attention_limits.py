@@ -55,3 +55,32 @@ def test_rows_of_a_cache_fit_a_slot(sffn):  # noqa: F811
     assert append(sffn, h, q=NONE, n_pages=1 << 27, page=16) == ARG
     assert append(sffn, h, q=NONE, n_pages=(1 << 27) + 1, page=16) == UNSUPPORTED
     assert append(sffn, h, q=NONE, n_pages=(1 << 31) - 1, page=(1 << 31) - 1) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("max_q", [1, 8, 16, 500])
+@pytest.mark.parametrize("window", [0, 5000])
+def test_workspace_under_the_limits_of_a_model(sffn, dtype, dim, max_q, window):  # noqa: F811
+    """max_kv is an upper bound and usually the model's limit: the partial results of single
+    tokens, drafts and chunks stay within 256 MiB (and its rounding) for every batch."""
+    import torch
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    for n_seqs in (1, 32, 64, 256, 512, 1024, 10000):
+        for max_kv in (4096, 32768, 131072, 1 << 20):
+            b = sffn.make_paged_batch(n_seqs * max_q, n_seqs, 32, 8, dim, dt, 16, 1 << 20, 1 << 16, max_q,
+                                      max_kv, window=window)
+            need = sffn.paged_attn_workspace_bytes(b)
+            assert need <= (256 << 20) + 1024, (n_seqs, max_kv, need)
+            # one sequence less than full: both kernels may have to run
+            b.T -= max_q - 1
+            assert sffn.paged_attn_workspace_bytes(b) <= 2 * (256 << 20) + 2048
+
+
+def test_workspace_holds_the_rows_that_exist(sffn):  # noqa: F811
+    """Single tokens of 4 heads a key head need 4 rows of partial results a split, not 32."""
+    import torch
+    b = sffn.make_paged_batch(32, 32, 32, 8, 128, torch.bfloat16, 16, 1 << 20, 1 << 16, 1, 4096)
+    one = 32 * 8 * 4 * (128 + 2) * 4     # 32 sequences, 8 key heads, output, maximum and sum
+    need = sffn.paged_attn_workspace_bytes(b)
+    assert need % one <= 512 and 2 <= need // one <= 8, need / one

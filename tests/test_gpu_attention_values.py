@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -133,3 +134,18 @@ def test_time_does_not_depend_on_what_lds_held():
             times.append(start.elapsed_time(end))
         medians.append(sorted(times)[7])
     assert medians[1] < 2 * medians[0], medians
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_sequences_under_the_limit_of_a_model(dtype):
+    """1100 sequences, most of them short, with max_kv far above them: the partial results are
+    limited, so that the few long ones are split less often than alone."""
+    rng = np.random.default_rng(40)
+    q_lens = [int(n) for n in rng.integers(1, 5, 1100)]
+    kv_lens = [int(n) for n in rng.integers(4, 60, 1100)]
+    for i, n in ((0, 20000), (500, 9500), (1099, 12001)):
+        kv_lens[i] = n
+    c = _attention_case(q_lens, kv_lens, 8, 1, 128, 16, dtype, seed=41)
+    c["bt"] = np.concatenate([c["bt"], np.full((1100, 8192 - c["bt"].shape[1]), -1, np.int32)], 1)
+    out, lse = _run(c, max_kv=131072)
+    _check_attention(c, out, lse)
