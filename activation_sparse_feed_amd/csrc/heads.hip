@@ -59,6 +59,15 @@ __device__ __forceinline__ float row_sum(float v, int G) {
   return v;
 }
 
+// 1 / sqrt(v) to 1 ulp.  The instruction takes a subnormal for 0, which would make
+// infinities of rows whose mean square is below 2^-126 (elements of 1e-19 with eps = 0): such
+// values are scaled by an even power of two first.
+__device__ __forceinline__ float inverse_root(float v) {
+  const bool tiny = v < 0x1p-96f;
+  const float r = __builtin_amdgcn_rsqf(tiny ? v * 0x1p60f : v);
+  return tiny ? r * 0x1p30f : r;
+}
+
 // The two chunks of this lane's unit u, element offsets o0 and o1 (o1 < 0:
 // none), and whether the unit exists and is rotated across its chunks.
 struct Unit {
@@ -249,7 +258,7 @@ __global__ __launch_bounds__(kHeadsBlock) void heads_fwd(HeadsFwd p) {
     ss = row_sum(ss, G);
     if (is_q || is_k) {
       if (p.norm) {
-        const float rs = __builtin_amdgcn_rsqf(ss * inv_d + p.eps);  // to 1 ulp
+        const float rs = inverse_root(ss * inv_d + p.eps);
         float wa[V], wb[V];
         Chunk<T, V>::unpack(is_q ? wq.a : wk.a, wa);
         Chunk<T, V>::unpack(is_q ? wq.b : wk.b, wb);
@@ -333,7 +342,7 @@ __global__ __launch_bounds__(kHeadsBlock) void heads_bwd(HeadsBwd p) {
       }
       ss = row_sum(ss, G);
       dot = row_sum(dot, G);
-      const float rs = __builtin_amdgcn_rsqf(ss * inv_d + p.eps);  // to 1 ulp
+      const float rs = inverse_root(ss * inv_d + p.eps);
       const float m = dot * rs * inv_d;  // mean of (gn w) xhat
 #pragma unroll
       for (int i = 0; i < V; ++i) {
