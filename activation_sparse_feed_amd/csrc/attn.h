@@ -50,8 +50,8 @@ struct PagedAttn {
   int T, n_seqs, hq, hkv, D, page_size, n_pages, max_pages, max_q, max_kv, causal, window;
   float scale;
 };
-bool paged_attn_fits(int dtype, const PagedAttn& p);  // into the grids of its launches
-size_t paged_attn_workspace(int dtype, const PagedAttn& p);
+// Whether p fits the grids of its launches, and the workspace that it needs.
+bool plan_paged_attn(int dtype, const PagedAttn& p, size_t* bytes);
 hipError_t launch_paged_attn(int dtype, const PagedAttn& p, void* ws, hipStream_t stream);
 
 }  // namespace sffn

@@ -95,7 +95,8 @@ PagedAttn attn_params(const sffn_paged_batch* b) {
   return p;
 }
 
-int32_t check_batch(const sffn_paged_batch* b) {
+// bytes: of the workspace, where the batch is taken.
+int32_t check_batch(const sffn_paged_batch* b, size_t* bytes) {
   if (b == nullptr) return SFFN_ERR_ARG;
   if (b->T < 0 || b->n_seqs < 0 || b->n_q_heads <= 0 || b->n_kv_heads <= 0 || b->head_dim <= 0 ||
       b->page_size <= 0 || b->n_pages < 0 || b->max_pages < 0 || b->max_q < 0 || b->max_kv < 0 ||
@@ -111,7 +112,7 @@ int32_t check_batch(const sffn_paged_batch* b) {
   if ((int64_t)b->T * b->n_q_heads > (1 << 30) || b->max_kv > (1 << 30) || b->n_seqs > (1 << 20) ||
       b->n_q_heads > 4096)
     return SFFN_ERR_UNSUPPORTED;
-  return paged_attn_fits(b->dtype, attn_params(b)) ? SFFN_OK : SFFN_ERR_UNSUPPORTED;
+  return plan_paged_attn(b->dtype, attn_params(b), bytes) ? SFFN_OK : SFFN_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -237,8 +238,8 @@ int32_t paged_kv_append(const sffn_heads* heads, const void* q, int64_t q_token,
 }
 
 size_t paged_attn_workspace_bytes(const sffn_paged_batch* batch) {
-  if (check_batch(batch) != SFFN_OK) return 0;
-  return paged_attn_workspace(batch->dtype, attn_params(batch));
+  size_t bytes = 0;
+  return check_batch(batch, &bytes) == SFFN_OK ? bytes : 0;
 }
 
 int32_t paged_attn_fwd(const sffn_paged_batch* batch, const void* q, int64_t q_token,
@@ -247,7 +248,8 @@ int32_t paged_attn_fwd(const sffn_paged_batch* batch, const void* q, int64_t q_t
                        int64_t vc_head, const int32_t* q_start, const int32_t* kv_len,
                        const int32_t* block_table, void* out, int64_t o_token, int64_t o_head,
                        float* lse, void* workspace, size_t ws_bytes, void* stream) {
-  int32_t st = check_batch(batch);
+  size_t need = 0;
+  int32_t st = check_batch(batch, &need);
   if (st != SFFN_OK) return st;
   const sffn_paged_batch& b = *batch;
   if (b.T == 0 || b.n_seqs == 0 || b.max_q == 0) return SFFN_OK;
@@ -267,7 +269,6 @@ int32_t paged_attn_fwd(const sffn_paged_batch* batch, const void* q, int64_t q_t
   p.k_cache = k_cache, p.kc_page = kc_page, p.kc_token = kc_token, p.kc_head = kc_head;
   p.v_cache = v_cache, p.vc_page = vc_page, p.vc_token = vc_token, p.vc_head = vc_head;
   p.q_start = q_start, p.kv_len = kv_len, p.block_table = block_table, p.lse = lse;
-  const size_t need = paged_attn_workspace(b.dtype, p);
   if (need > 0 && (!given(workspace, 16) || ws_bytes < need)) return SFFN_ERR_WORKSPACE;
   return hip_status(launch_paged_attn(b.dtype, p, workspace, (hipStream_t)stream));
 }

@@ -186,21 +186,20 @@ hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipS
 // A grid has less than 2^32 threads in x: workgroups of attn_rows and of both joins
 // have 256, those of attn_keys 64 a wave.  Where attn_keys numbers its items itself,
 // the numbers (and one step of the grid past them) are 32-bit.
-bool paged_attn_fits(int dtype, const PagedAttn& p) {
+bool plan_paged_attn(int dtype, const PagedAttn& p, size_t* bytes) {
+  *bytes = 0;
+  if (p.T == 0 || p.n_seqs == 0 || p.max_q == 0) return true;  // nothing is launched
   const Plan keys = plan_keys(dtype, p), rows = plan_rows(dtype, p, keys.used);
-  const int64_t most = ((int64_t)1 << 32) - 1;
+  const int64_t most = ((int64_t)1 << 32) - 1, wgs = (int64_t)keys.tiles * p.hkv;
   if (rows.used && (int64_t)rows.tiles * p.hkv * 256 > most) return false;
-  if (!keys.used) return true;
-  const int64_t wgs = (int64_t)keys.tiles * p.hkv;
-  if (keys.splits > 1 && wgs * 256 > most) return false;
-  return rows.used ? wgs * keys.splits <= (1ll << 31) - 1 - 2 * kCus
-                   : wgs * attn_keys_waves(dtype == 1 ? 2 : 4, p.D) * kWave <= most;
-}
-
-size_t paged_attn_workspace(int dtype, const PagedAttn& p) {
-  if (p.T == 0 || p.n_seqs == 0 || p.max_q == 0) return 0;
-  const Plan keys = plan_keys(dtype, p);
-  return keys.bytes + plan_rows(dtype, p, keys.used).bytes;
+  if (keys.used) {
+    if (keys.splits > 1 && wgs * 256 > most) return false;
+    if (rows.used ? wgs * keys.splits > (1ll << 31) - 1 - 2 * kCus
+                  : wgs * attn_keys_waves(dtype == 1 ? 2 : 4, p.D) * kWave > most)
+      return false;
+  }
+  *bytes = keys.bytes + rows.bytes;
+  return true;
 }
 
 hipError_t launch_paged_attn(int dtype, const PagedAttn& p, void* ws, hipStream_t stream) {

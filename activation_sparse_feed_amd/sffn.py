@@ -430,14 +430,34 @@ def _cache(name: str, t, n_pages: int, page_size: int, heads: int, dim: int, dty
     return t.data_ptr(), s0, s1, s2
 
 
-def _array(name: str, t, n: int, dtype):
-    """Pointer of a contiguous array of at least n elements (None: absent)."""
+def _array(name: str, t, n: int, dtype, exact: bool = False):
+    """Pointer of a contiguous array of at least n elements (None: absent), exact: of n, as
+    one row of norm weights for all heads."""
     if t is None:
         return None
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.numel() < n:
-        raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
+    size = t.numel()
+    if size < n or (exact and size > n):
+        raise ValueError(f"{name} must have {n} elements, not {size}")
+    return _pointer(t)
+
+
+def _table(name: str, t, rows: int, cols: int, dtype):
+    """The same of a table [rows or more, cols], or flat: the kernels step over rows of
+    cols elements."""
+    if t is None:
+        return None
+    if t.shape != (rows, cols):
+        if t.dim() == 2 and t.shape[1] != cols:
+            raise ValueError(f"{name} must have {cols} columns, not {t.shape[1]}")
+        return _array(name, t, rows * cols, dtype)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    return _pointer(t)
+
+
+def _pointer(t):
     if not t.is_cuda:
         raise ValueError("tensors must live on the GPU")
     if not t.is_contiguous():
@@ -445,24 +465,11 @@ def _array(name: str, t, n: int, dtype):
     return t.data_ptr()
 
 
-def _weight(name: str, t, dim: int, dtype):
-    """Pointer of a norm's weights or their gradients: one row for all heads."""
-    if t is not None and t.numel() != dim:
-        raise ValueError(f"{name} must have {dim} elements, not {t.numel()}")
-    return _array(name, t, dim, dtype)
-
-
-def _columns(name: str, t, cols: int):
-    """The kernels step over rows of `cols` elements: a table with others would be misread."""
-    if t is not None and t.dim() == 2 and t.shape[1] != cols:
-        raise ValueError(f"{name} must have {cols} columns, not {t.shape[1]}")
-
-
 def _rotation(h: Heads, q_weight, k_weight, table, positions, dt):
     if h.rot_dim and table is not None and table.dim() == 2 and table.shape[1] != h.rot_dim:
         raise ValueError(f"the rotation table must be [max_pos, {h.rot_dim}]")
-    return (_weight("q_weight", q_weight, h.head_dim, dt),
-            _weight("k_weight", k_weight, h.head_dim, dt),
+    return (_array("q_weight", q_weight, h.head_dim, dt, True),
+            _array("k_weight", k_weight, h.head_dim, dt, True),
             _array("the rotation table", table, h.max_pos * h.rot_dim, torch.float32),
             _array("positions", positions, h.T, torch.int32))
 
@@ -511,8 +518,8 @@ def qk_norm_rope_bwd(heads: Heads, q, k, q_weight, k_weight, table, positions, g
         *_rotation(heads, q_weight, k_weight, table, positions, dt),
         *_rows("gq_out", gq_out, T, nq, D, dt), *_rows("gk_out", gk_out, T, nk, D, dt),
         *_rows("gq", gq, T, nq, D, dt), *_rows("gk", gk, T, nk, D, dt),
-        _weight("gq_weight", gq_weight, D, torch.float32),
-        _weight("gk_weight", gk_weight, D, torch.float32), ws, ws_n,
+        _array("gq_weight", gq_weight, D, torch.float32, True),
+        _array("gk_weight", gk_weight, D, torch.float32, True), ws, ws_n,
         _stream_ptr(stream, gq_out if nq else gk_out)))
 
 
@@ -551,8 +558,6 @@ def paged_attn_fwd(batch: PagedBatch, q, k_cache, v_cache, q_start, kv_len, bloc
     its kv_len[s] cached keys, found through block_table [n_seqs, max_pages]."""
     T, D, dt = batch.T, batch.head_dim, _TORCH_DTYPE[batch.dtype]
     nq, nk, ns = batch.n_q_heads, batch.n_kv_heads, batch.n_seqs
-    _columns("block_table", block_table, batch.max_pages)
-    _columns("lse", lse, nq)
     ws, ws_n = (None, 0) if workspace is None else \
         (_ptr(workspace), workspace.numel() * workspace.element_size())
     _check("paged_attn_fwd", _lib.paged_attn_fwd(
@@ -560,8 +565,8 @@ def paged_attn_fwd(batch: PagedBatch, q, k_cache, v_cache, q_start, kv_len, bloc
         *_cache("k_cache", k_cache, batch.n_pages, batch.page_size, nk, D, dt),
         *_cache("v_cache", v_cache, batch.n_pages, batch.page_size, nk, D, dt),
         _array("q_start", q_start, ns + 1, torch.int32), _array("kv_len", kv_len, ns, torch.int32),
-        _array("block_table", block_table, ns * batch.max_pages, torch.int32),
-        *_rows("out", out, T, nq, D, dt), _array("lse", lse, T * nq, torch.float32), ws, ws_n,
+        _table("block_table", block_table, ns, batch.max_pages, torch.int32),
+        *_rows("out", out, T, nq, D, dt), _table("lse", lse, T, nq, torch.float32), ws, ws_n,
         _stream_ptr(stream, out)))
 
 
