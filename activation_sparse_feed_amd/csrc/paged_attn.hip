@@ -209,10 +209,10 @@ hipError_t launch_paged_attn(int dtype, const PagedAttn& p, void* ws, hipStream_
   a.g = p.hq / p.hkv;
   a.page = FastDiv::make(p.page_size);
   a.group = FastDiv::make(a.g);
-  // scores are scaled in the exponent; a scale of 0 becomes one that leaves every
-  // weight 1 but keeps hidden keys at -inf
+  // scores are scaled in the exponent; a scale of 0 becomes the smallest number, which
+  // leaves every weight 1 but keeps hidden keys at -inf
   const float c = (p.scale < 0.f ? -p.scale : p.scale) * 1.44269504088896340736f;
-  a.c = c > 0x1p-90f ? c : 0x1p-90f;
+  a.c = c > 0.f ? c : 0x1p-149f;
   a.negate = p.scale < 0.f;
   return dtype == 1 ? launch<uint16_t>(a, keys, rows, ws, stream)
                     : launch<float>(a, keys, rows, ws, stream);

@@ -149,3 +149,16 @@ def test_many_sequences_under_the_limit_of_a_model(dtype):
     c["bt"] = np.concatenate([c["bt"], np.full((1100, 8192 - c["bt"].shape[1]), -1, np.int32)], 1)
     out, lse = _run(c, max_kv=131072)
     _check_attention(c, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 3], [90, 5000]), ([100], [130])])
+@pytest.mark.parametrize("size,sm_scale", [(1e14, 1e-29), (1e14, -3e-29), (1e18, 0.0), (1e17, 1e-35)])
+def test_very_small_scales(q_lens, kv_lens, size, sm_scale, dtype):
+    """Scores count after their scale, however small it is: products of 1e29 times 1e-29, and
+    a scale of 0, which makes every key's weight the same, with products of 1e36."""
+    c = _attention_case(q_lens, kv_lens, 4, 2, 64, 16, dtype, seed=50, scale=size)
+    finite = torch.isfinite(c["k"])
+    c["k"] = torch.where(finite, c["k"] * size, c["k"])
+    out, lse = _run(c, sm_scale=sm_scale)
+    _check_attention(c, out, lse, sm_scale=sm_scale)
