@@ -572,10 +572,13 @@ def paged_attn_fwd(batch: PagedBatch, q, k_cache, v_cache, q_start, kv_len, bloc
 
 def paged_slots(block_table, seq, positions, page_size: int) -> torch.Tensor:
     """Slots (int32) of tokens at `positions` of the sequences `seq`, through
-    block_table; computed once a step, for all layers."""
+    block_table; computed once a step, for all layers.  -1 (not stored) for positions
+    outside the table, as -1 for padding tokens, and for pages that are not there (-1)."""
     pos = positions.long()
+    inside = (pos >= 0) & (pos < block_table.shape[1] * page_size)
+    pos = torch.where(inside, pos, 0)
     page = block_table[seq.long(), pos // page_size].long()
-    return (page * page_size + pos % page_size).to(torch.int32)
+    return torch.where(inside & (page >= 0), page * page_size + pos % page_size, -1).to(torch.int32)
 
 
 class PagedAttention:

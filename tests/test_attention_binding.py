@@ -106,3 +106,12 @@ def test_tensors_of_another_device(sffn, monkeypatch):  # noqa: F811
             call(sffn)
         here = 1
         accepted(sffn, call)
+
+
+def test_slots_of_tokens_outside_the_table(sffn):  # noqa: F811
+    """Padding tokens get no slot, not the last page's."""
+    bt = torch.tensor([[4, 2, 7], [1, 0, -1]], dtype=torch.int32)
+    seq = torch.tensor([0, 0, 0, 0, 0, 1, 1])
+    pos = torch.tensor([-1, -15, 14, 15, 1 << 30, 3, 11])
+    assert sffn.paged_slots(bt, seq, pos, 5).tolist() == [-1, -1, 39, -1, -1, 8, -1]
+    assert sffn.paged_slots(bt, seq.int(), pos.int(), 5).dtype is torch.int32
