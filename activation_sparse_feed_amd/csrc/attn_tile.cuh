@@ -1,5 +1,5 @@
 // Attention over a paged cache on matrix instructions: the tile shared by the
-// kernels of paged_attn.cuh.
+// kernels of attn_kernels.cuh.
 //
 // A wave holds 32 query rows and walks over keys in blocks of 32, transposed:
 //   S^T [key, row] = K Q^T      O^T [d, row] += V^T P^T
@@ -244,12 +244,15 @@ struct AttnTile {
     return __builtin_bit_cast(u32x4_t, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
   }
 
-  // o += V^T P^T over the 32 keys at v.
+  // o += V^T P^T over the 32 keys at v.  In bf16 the weights are rounded to bf16 here,
+  // since the matrix instruction takes both operands in one type; their sum l is that of the
+  // unrounded ones, and o is float32.  Relative error against 64 bits 2.0e-3 to 2.3e-3,
+  // where rounding the output alone gives 1.5e-3 to 1.7e-3 (standard normal inputs).
   __device__ __forceinline__ void accumulate(const uint8_t* v, const f32x16_t& s) {
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        u32x4_t pf;  // the weights are rounded to the type of V here
+        u32x4_t pf;
 #pragma unroll
         for (int j = 0; j < 4; ++j) pf[j] = pack_bf16(s[8 * ks + 2 * j], s[8 * ks + 2 * j + 1]);
 #pragma unroll
@@ -281,7 +284,8 @@ struct AttnTile {
   // A key that a row does not see has weight 0, but 0 times an infinite or NaN
   // value is NaN.  So in tiles with hidden keys such values are looked for, and
   // if there are any, added directly to the outputs of the rows that see them
-  // (add_infinite) and replaced by 0 in LDS (clear_infinite).
+  // (add_infinite) and replaced by 0 in LDS (clear_infinite).  The search runs over
+  // whole LDS rows, so what lies in them beyond head_dim has to be finite.
   // The 16-byte chunks of the tile are shared by N threads, this being thread i.
   __device__ static __forceinline__ bool infinite_bits(u32x4_t x) {
     bool bad = false;

@@ -6,7 +6,9 @@
 // where the pairing of the rotation allows it.  At 16384 tokens of 32 + 8 heads of
 // 128, bf16: forward 68 us for 344 MB (5.0 TB/s; a large copy runs at 4.8),
 // backward 110 us for 512 MB (4.7 TB/s), append 82 us for 408 MB.  A decode step
-// of 32 tokens takes 4.3 us, the latency of its dependent loads.  A row is held by G lanes
+// of 32 tokens takes 4.4 us, the latency of its dependent loads.  In float32, 4000
+// tokens of the same heads: forward 38 us (4.4 TB/s), append 45 us (4.5 TB/s), backward
+// 56 us (4.5 TB/s).  A row is held by G lanes
 // (a power of two), each with two chunks of V elements: for pairs
 // (i, i + rot/2) the chunks that are partners of each other, so that the
 // rotation needs no data of other lanes; a wave holds 64 / G rows of one
@@ -447,10 +449,13 @@ int lanes_per_row(int D, int rot, bool adjacent, int V) {
   return g;  // at most 64: head_dim <= 256 and V >= 2
 }
 
-// Blocks of the backward: two waves a SIMD, which is what its registers allow, all
-// resident at once (256: 148 us at 16384 tokens, 512: 120, 768: 140, 1024: 128;
-// 110 since).  One pass a wave for few tokens took 1.4 us off 33 tokens (19.1), but
-// added 6 us here.
+// Blocks of the backward: two waves a SIMD, which is what the registers of the instance
+// with the widest chunks allow (197), all resident at once.  512 / 768 / 1024 blocks, in us:
+// 16384 bf16 tokens of 32 + 8 heads of 128 115 / 135 / 121, of 16 + 4 of 80 with
+// adjacent pairs 73 / 93 / 82, 4000 float32 tokens of 32 + 8 of 128 57 / 61 / 62.  Instances
+// of narrower chunks hold four waves a SIMD and lose by it: bf16, 80 wide, 40 rotated
+// 65 / 53 / 49, float32, 80 wide, 40 rotated in adjacent pairs 83 / 74 / 73.  One pass a
+// wave for few tokens took 1.4 us off 33 tokens (19.1), but added 6 us at 16384.
 int bwd_blocks(int T) {
   const int need = (T + kHeadsBlock / kWave - 1) / (kHeadsBlock / kWave);
   return need < 512 ? need : 512;
@@ -490,7 +495,10 @@ hipError_t launch_heads_fwd(int dtype, HeadsFwd p, hipStream_t stream) {
   const int passes = (rows + rpw - 1) / rpw;
   // few tokens: a wave for every pass over a token's heads, so that the rows
   // of a decode step are read side by side; many: one wave per token, which
-  // keeps the angles
+  // keeps the angles.  A wave for every pass / one per token, in us: norm of 32 + 8 heads
+  // of 128, bf16, 256 tokens 3.9 / 7.5, 1024 7.2 / 9.8, 2047 10.6 / 11.1, 4096 22.0 / 20.8,
+  // 16384 80.5 / 69.0; append 32 tokens 3.6 / 7.9, 4096 26.8 / 25.5; float32, 16 + 4 heads of
+  // 80, 512 tokens 3.9 / 5.7, 4096 13.1 / 11.5; but 32 + 8 of 128, 4000 37.2 / 37.9
   const int per_wave = p.T < 2048 ? 1 : passes;
   p.rows_per_wave = per_wave * rpw;
   const dim3 grid((unsigned)((p.T + 3) / 4), (unsigned)((passes + per_wave - 1) / per_wave));

@@ -544,7 +544,8 @@ typedef struct {
   int32_t max_q;      /* no sequence has more new tokens */
   int32_t max_kv;     /* no sequence is longer; at most max_pages * page_size */
   int32_t causal;     /* 1: a token sees no later key; 0: it does */
-  int32_t window;     /* > 0: a token sees no key `window` or more before it; 0: no limit */
+  int32_t window;     /* > 0: a token sees no key `window` or more before it; 0, or max_kv
+                         and more: no limit */
   float scale;        /* of the scores, finite */
   int32_t dtype;      /* sffn_dtype */
 } sffn_paged_batch;
@@ -570,9 +571,15 @@ typedef struct {
  * 0 .. n_pages - 1.  (These arrays are on the device and cannot be checked on
  * the host: the kernels bound every value, so a wrong one gives wrong
  * results but no access outside the buffers.)  Cache rows that a row does not
- * see may hold anything, NaN included: they do not change its result.
+ * see may hold anything, NaN included: they do not change its result.  An
+ * infinite or NaN element of a value that it sees makes that element of its
+ * result infinite or NaN (NaN for an infinite one whose weight is below
+ * float32's range).
  * out: as q.  lse: float32 [T, n_q_heads] or NULL.
- * workspace: at least paged_attn_workspace_bytes(batch); no initial contents.
+ * workspace: at least paged_attn_workspace_bytes(batch), about 256 MiB at most
+ * for each of the two kernels that a batch may take; no initial contents.
+ * max_q and max_kv set it and how far key ranges are split, so bounds near the
+ * batch's lengths are faster.
  * Weights of the bf16 softmax are rounded to bf16 before the product with v;
  * sums and the running maximum are float32.  Results do not depend on the order
  * in which workgroups run: the same call gives the same bits.
