@@ -19,7 +19,9 @@ BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "twell_gate.hip", "convert.hip", "dense.hip", "dense_skinny.hip", "sparse.hip",
            "route.hip", "norms.hip", "union.hip", "backward.hip", "backward_routed.hip", "probe.hip",
            "attn_api.hip", "heads.hip", "paged_attn.hip", "attn_rows_bf16.hip", "attn_rows_f32.hip",
-           "attn_keys_bf16.hip", "attn_keys_f32.hip"]
+           "attn_keys_bf16.hip", "attn_keys_f32.hip", "attn_mx4_api.hip", "heads_mx4.hip",
+           "paged_attn_mx4.hip", "attn_mx4_rows_bf16.hip", "attn_mx4_rows_f32.hip",
+           "attn_mx4_keys_bf16.hip", "attn_mx4_keys_f32.hip"]
 ARCH = os.environ.get("SFFN_OFFLOAD_ARCH", "gfx950")
 
 # Packed-FP32 instructions are kept out of the generated code.

@@ -54,4 +54,29 @@ struct PagedAttn {
 bool plan_paged_attn(int dtype, const PagedAttn& p, size_t* bytes);
 hipError_t launch_paged_attn(int dtype, const PagedAttn& p, void* ws, hipStream_t stream);
 
+// ---------------------------------------------------------------- the 4-bit cache
+// One cache (K or V): codes and scale bytes, strides in bytes.
+struct Mx4Rows {
+  uint8_t *codes, *scales;
+  int64_t page, token, head, s_page, s_token, s_head;
+};
+
+// p: as for the append, its k_out, v_out and their strides unused.
+hipError_t launch_heads_mx4(int dtype, HeadsFwd p, Mx4Rows k, Mx4Rows v, hipStream_t stream);
+
+// out null: not read.
+struct Mx4Read {
+  Mx4Rows cache[2];   // K, V
+  const int32_t* slots;
+  void* out[2];
+  int64_t o_token[2], o_head[2];
+  int T, hkv, D, n_pages, page_size;
+};
+hipError_t launch_mx4_read(int dtype, const Mx4Read& p, hipStream_t stream);
+
+// p: as for paged_attn, its caches and their strides unused.
+bool plan_paged_attn_mx4(int dtype, const PagedAttn& p, size_t* bytes);
+hipError_t launch_paged_attn_mx4(int dtype, const PagedAttn& p, const Mx4Rows& k, const Mx4Rows& v,
+                                 void* ws, hipStream_t stream);
+
 }  // namespace sffn

@@ -225,6 +225,91 @@ __device__ __forceinline__ float finish_lse(float m, float l) {
   return l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
 }
 
+// The place of a workgroup of attn_rows: its tile of TM rows of a sequence, its keys, and
+// this lane's row.
+struct RowsPlace {
+  Work w;
+  int wave, r0, r1;            // first and last row of the tile
+  int b, e, n_split;           // keys of this split, splits of the tile
+  int x, y;                    // keys that all rows of the tile see
+  int r, token, head;          // this lane's row
+  int row_lo, row_hi;          // the keys that it sees
+  int w_lo0, w_hi0, w_lo1, w_hi1;  // those of the wave's first and last row
+  bool wave_live;
+
+  // False: nothing to do.
+  template <int TM>
+  __device__ __forceinline__ bool init(const AttnArgs& a, int t, int hk, int split) {
+    const PagedAttn& p = a.p;
+    w = find_tile<TM>(a, t);
+    if (w.tile < 0) return false;
+    wave = uniform((int)threadIdx.x / kWave);
+    const int lane = lane_id(), rows = w.nq * a.g;
+    r0 = w.tile * TM, r1 = min(r0 + TM, rows) - 1;
+    int lo, hi;
+    key_range(p, w, a.group.div(r0), &lo, &y);
+    key_range(p, w, a.group.div(r1), &x, &hi);
+    n_split = split_range(a, split, lo, hi, &b, &e);
+    if (split >= n_split) return false;
+    const int wr0 = min(r0 + wave * 32, rows - 1), wr1 = min(wr0 + 31, r1);
+    r = min(r0 + wave * 32 + (lane & 31), r1);
+    token = a.group.div(r), head = hk * a.g + r - token * a.g;
+    key_range(p, w, token, &row_lo, &row_hi);
+    key_range(p, w, a.group.div(wr0), &w_lo0, &w_hi0);
+    key_range(p, w, a.group.div(wr1), &w_lo1, &w_hi1);
+    wave_live = r0 + wave * 32 <= r1;
+    return true;
+  }
+  __device__ __forceinline__ int64_t q_offset(const PagedAttn& p) const {
+    return (int64_t)(w.q0 + token) * p.q_token + head * p.q_head;
+  }
+  // Of the 32 keys from j on, the wave's rows see none; all.
+  __device__ __forceinline__ bool sees_none(int j) const { return !wave_live || j >= w_hi1 || j + 32 <= w_lo0; }
+  __device__ __forceinline__ bool sees_all(int j) const { return j >= w_lo1 && j + 32 <= w_hi0; }
+};
+
+// The wave's rows of such a tile, result or part of a split.
+template <typename T, int TM, typename Tile>
+__device__ __forceinline__ void write_rows(const AttnArgs& a, const RowsPlace& pl, Tile& tile, int t, int hk,
+                                           int split) {
+  const PagedAttn& p = a.p;
+  const int lane = lane_id(), half = lane >> 5;
+  tile.l = sum_halves(tile.l);
+  const float m = tile.m * a.c;
+  if (pl.r0 + pl.wave * 32 + (lane & 31) > pl.r1) return;
+  if (pl.n_split == 1) {
+    const float inv = tile.l == 0.f ? 0.f : 1.f / tile.l;
+    T* out = (T*)p.out + (int64_t)(pl.w.q0 + pl.token) * p.o_token + pl.head * p.o_head;
+#pragma unroll
+    for (int d = 0; d < Tile::kDt; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = d * 32 + 8 * i + 4 * half;
+        if (at < p.D)
+          store4<T>(out + at, tile.o[d][4 * i] * inv, tile.o[d][4 * i + 1] * inv,
+                    tile.o[d][4 * i + 2] * inv, tile.o[d][4 * i + 3] * inv);
+      }
+    if (p.lse != nullptr && half == 0)
+      p.lse[(int64_t)(pl.w.q0 + pl.token) * p.hq + pl.head] = finish_lse(m, tile.l);
+  } else {
+    const size_t slot = split * a.part_rows + ((size_t)t * p.hkv + hk) * TM + (pl.r - pl.r0);
+    float* out = a.part_o + slot * p.D;
+#pragma unroll
+    for (int d = 0; d < Tile::kDt; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = d * 32 + 8 * i + 4 * half;
+        if (at < p.D)
+          store4<float>(out + at, tile.o[d][4 * i], tile.o[d][4 * i + 1], tile.o[d][4 * i + 2],
+                        tile.o[d][4 * i + 3]);
+      }
+    if (half == 0) {
+      a.part_ml[2 * slot] = m;
+      a.part_ml[2 * slot + 1] = tile.l;
+    }
+  }
+}
+
 template <typename T, int DP, int KT, int NW, int G>
 __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void attn_rows(AttnArgs a) {
   typedef AttnTile<T, DP, KT> Tile;
@@ -244,26 +329,9 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
   if (DP <= 128 && all <= 2 * kCus && id >= kCus) id = all - 1 - (id - kCus);
   const int split = id / (int)gridDim.x, th = id - split * (int)gridDim.x;
   const int hk = th % p.hkv, t = th / p.hkv;
-  const Work w = find_tile<TM>(a, t);
-  if (w.tile < 0) return;
-  const int wave = uniform((int)threadIdx.x / kWave), lane = lane_id(), half = lane >> 5;
-  const int rows = w.nq * a.g;
-  const int r0 = w.tile * TM, r1 = min(r0 + TM, rows) - 1;  // first and last row of the tile
-  int lo, hi, b, e, x, y;
-  key_range(p, w, a.group.div(r0), &lo, &y);
-  key_range(p, w, a.group.div(r1), &x, &hi);
-  const int n_split = split_range(a, split, lo, hi, &b, &e);
-  if (split >= n_split) return;
-  // this lane's row, and the ranges of the wave's first and last row
-  const int wr0 = min(r0 + wave * 32, rows - 1), wr1 = min(wr0 + 31, r1);
-  const int r = min(r0 + wave * 32 + (lane & 31), r1);
-  const int token = a.group.div(r), head = hk * a.g + r - token * a.g;
-  int row_lo, row_hi, w_lo0, w_hi0, w_lo1, w_hi1;
-  key_range(p, w, token, &row_lo, &row_hi);
-  key_range(p, w, a.group.div(wr0), &w_lo0, &w_hi0);
-  key_range(p, w, a.group.div(wr1), &w_lo1, &w_hi1);
-  const bool wave_live = r0 + wave * 32 <= r1;
-
+  RowsPlace pl;
+  if (!pl.template init<TM>(a, t, hk, split)) return;
+  const int wave = pl.wave, b = pl.b, e = pl.e, x = pl.x, y = pl.y, row_lo = pl.row_lo, row_hi = pl.row_hi;
   Tile tile;
   tile.init();
   // chunks that no load writes, but that are read: up to DP by the products, up to the
@@ -278,9 +346,9 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
   static_assert(kPer >= 1, "");
   TileLoader<T, DP, KT, G, kPer, true> load_k;
   TileLoader<T, DP, KT, G, kPer, false> load_v;
-  load_k.init(a, w.seq, hk, b, e, wave * kPer);
-  load_v.init(a, w.seq, hk, b, e, wave * kPer);
-  const T* q = (const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head;
+  load_k.init(a, pl.w.seq, hk, b, e, wave * kPer);
+  load_v.init(a, pl.w.seq, hk, b, e, wave * kPer);
+  const T* q = (const T*)p.q + pl.q_offset(p);
   // The K tile that is in LDS beside a V tile is 32 keys ahead of it: step()
   // needs the next block's K with a block's V.
   f32x16_t s;
@@ -320,10 +388,10 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
     for (int i = 0; i < KT / 32; ++i) {
       const int j = j0 + i * 32;
       // the wave's rows see none of the block's keys, or not all of them
-      if (!wave_live || j >= w_hi1 || j + 32 <= w_lo0) {
+      if (pl.sees_none(j)) {
         s = tile.scores(k + i * Tile::kBlockBytes);
       } else {
-        if (j < w_lo1 || j + 32 > w_hi0) Tile::hide(s, j, row_lo, row_hi);
+        if (!pl.sees_all(j)) Tile::hide(s, j, row_lo, row_hi);
         tile.step(s, k + i * Tile::kBlockBytes, v + i * Tile::kBlockBytes, a.c);
       }
     }
@@ -334,40 +402,7 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
     if (j0 >= e) break;
     iteration(k1, v1, k0, v0);
   }
-  tile.l = sum_halves(tile.l);
-  const float m = tile.m * a.c;
-  if (r0 + wave * 32 + (lane & 31) > r1) return;
-  if (n_split == 1) {
-    const float inv = tile.l == 0.f ? 0.f : 1.f / tile.l;
-    T* out = (T*)p.out + (int64_t)(w.q0 + token) * p.o_token + head * p.o_head;
-#pragma unroll
-    for (int d = 0; d < Tile::kDt; ++d)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = d * 32 + 8 * i + 4 * half;
-        if (at < p.D)
-          store4<T>(out + at, tile.o[d][4 * i] * inv, tile.o[d][4 * i + 1] * inv,
-                    tile.o[d][4 * i + 2] * inv, tile.o[d][4 * i + 3] * inv);
-      }
-    if (p.lse != nullptr && half == 0)
-      p.lse[(int64_t)(w.q0 + token) * p.hq + head] = finish_lse(m, tile.l);
-  } else {
-    const size_t slot = split * a.part_rows + ((size_t)t * p.hkv + hk) * TM + (r - r0);
-    float* out = a.part_o + slot * p.D;
-#pragma unroll
-    for (int d = 0; d < Tile::kDt; ++d)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = d * 32 + 8 * i + 4 * half;
-        if (at < p.D)
-          store4<float>(out + at, tile.o[d][4 * i], tile.o[d][4 * i + 1], tile.o[d][4 * i + 2],
-                        tile.o[d][4 * i + 3]);
-      }
-    if (half == 0) {
-      a.part_ml[2 * slot] = m;
-      a.part_ml[2 * slot + 1] = tile.l;
-    }
-  }
+  write_rows<T, TM>(a, pl, tile, t, hk, split);
 }
 
 template <typename T, int DP, int NW, int G, bool COMPACT>

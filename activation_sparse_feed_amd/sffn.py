@@ -30,7 +30,9 @@ EXPORTED = ("twell_weight_norms", "twell_pack", "twell_pack_noalloc",
             "sffn_probe_cached", "sffn_probe_gather", "sffn_probe_bf16_round",
             "sffn_workspace_bytes", "sparse_ffn_bwd_workspace_bytes", "sffn_strerror",
             "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes",
-            "paged_kv_append", "paged_attn_fwd", "paged_attn_workspace_bytes")
+            "paged_kv_append", "paged_attn_fwd", "paged_attn_workspace_bytes",
+            "paged_kv_append_mx4", "paged_kv_read_mx4", "paged_attn_mx4_fwd",
+            "paged_attn_mx4_workspace_bytes")
 
 
 class SffnError(RuntimeError):
@@ -55,6 +57,12 @@ class PagedBatch(ctypes.Structure):
                 ("T", "n_seqs", "n_q_heads", "n_kv_heads", "head_dim", "page_size", "n_pages",
                  "max_pages", "max_q", "max_kv", "causal", "window")] + \
                [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class Mx4Rows(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int64) for n in ("page", "token", "head", "scale_page", "scale_token",
+                                              "scale_head")]
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -97,7 +105,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qk_norm_rope_bwd.argtypes = [hp] + rows * 2 + [vp] * 4 + rows * 4 + [vp] * 3 + [sz, vp]
     lib.paged_kv_append.argtypes = [hp] + rows * 3 + [vp] * 5 + rows + cache * 2 + [i32, i32, vp]
     lib.paged_attn_fwd.argtypes = [bp] + rows + cache * 2 + [vp] * 3 + rows + [vp, vp, sz, vp]
-    for fn in ("qk_norm_rope", "qk_norm_rope_bwd", "paged_kv_append", "paged_attn_fwd"):
+    mp = ctypes.POINTER(Mx4Rows)
+    lib.paged_kv_append_mx4.argtypes = [hp] + rows * 3 + [vp] * 5 + rows + [mp, mp, i32, i32, vp]
+    lib.paged_kv_read_mx4.argtypes = [i32] * 4 + [mp, mp, i32, i32, vp] + rows * 2 + [vp]
+    lib.paged_attn_mx4_fwd.argtypes = [bp] + rows + [mp, mp] + [vp] * 3 + rows + [vp, vp, sz, vp]
+    lib.paged_attn_mx4_workspace_bytes.argtypes = [bp]
+    lib.paged_attn_mx4_workspace_bytes.restype = sz
+    for fn in ("qk_norm_rope", "qk_norm_rope_bwd", "paged_kv_append", "paged_attn_fwd",
+               "paged_kv_append_mx4", "paged_kv_read_mx4", "paged_attn_mx4_fwd"):
         getattr(lib, fn).restype = i32
     lib.qk_norm_rope_bwd_workspace_bytes.argtypes = [hp]
     lib.qk_norm_rope_bwd_workspace_bytes.restype = sz
@@ -425,7 +440,7 @@ def _cache(name: str, t, n_pages: int, page_size: int, heads: int, dim: int, dty
     if not t.is_cuda:
         raise ValueError("tensors must live on the GPU")
     s0, s1, s2, s3 = t.stride()
-    if s3 != 1:
+    if s3 != 1 and dim > 1:
         raise ValueError(f"{name}: head_dim must be contiguous")
     return t.data_ptr(), s0, s1, s2
 
@@ -568,6 +583,105 @@ def paged_attn_fwd(batch: PagedBatch, q, k_cache, v_cache, q_start, kv_len, bloc
         _table("block_table", block_table, ns, batch.max_pages, torch.int32),
         *_rows("out", out, T, nq, D, dt), _table("lse", lse, T, nq, torch.float32), ws, ws_n,
         _stream_ptr(stream, out)))
+
+
+class Mx4Cache:
+    """A layer's keys and values in four bits (OCP MX FP4, blocks of 32 elements of a head):
+    codes uint8 [n_pages, page_size, n_kv_heads, head_dim / 2] and scales uint8 [n_pages,
+    page_size, n_kv_heads, ceil(head_dim / 32)] of each, any strides with the last dimension
+    contiguous.  Allocated here, a page's tokens of one head lie side by side.  The tensors
+    are the cache's own: they keep their places for its lifetime."""
+
+    def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda",
+                 k_codes=None, k_scales=None, v_codes=None, v_scales=None):
+        self.n_pages, self.page_size = int(n_pages), int(page_size)
+        self.n_kv_heads, self.head_dim = int(n_kv_heads), int(head_dim)
+        if self.head_dim <= 0 or self.head_dim % 8:
+            raise ValueError(f"head_dim must be a positive multiple of 8, not {head_dim}")
+        given = (k_codes, k_scales, v_codes, v_scales)
+        if any(t is None for t in given):
+            if any(t is not None for t in given):
+                raise ValueError("codes and scales of k and v are given together or not at all")
+            given = [torch.zeros((self.n_pages, self.n_kv_heads, self.page_size, n),
+                                 dtype=torch.uint8, device=device).transpose(1, 2)
+                     for n in (self.head_dim // 2, -(-self.head_dim // 32)) * 2]
+        self._tensors = tuple(given)
+        self._k = self._place("k", *given[:2])
+        self._v = self._place("v", *given[2:])
+        if len({t.device for t in given}) > 1:
+            raise ValueError("the tensors of a cache must lie on one GPU")
+
+    def _place(self, name, codes, scales) -> Mx4Rows:
+        shape = self.n_pages, self.page_size, self.n_kv_heads
+        c = _cache(name + "_codes", codes, *shape, self.head_dim // 2, torch.uint8)
+        s = _cache(name + "_scales", scales, *shape, -(-self.head_dim // 32), torch.uint8)
+        return Mx4Rows(c[0], s[0], *c[1:], *s[1:])
+
+    k_codes = property(lambda self: self._tensors[0])
+    k_scales = property(lambda self: self._tensors[1])
+    v_codes = property(lambda self: self._tensors[2])
+    v_scales = property(lambda self: self._tensors[3])
+
+    def _check(self, fn: str, n_pages: int, page_size: int, heads: int, dim: int) -> None:
+        if (n_pages, page_size, heads, dim) != (self.n_pages, self.page_size, self.n_kv_heads,
+                                                self.head_dim):
+            raise ValueError(f"{fn}: the cache has {self.n_pages} pages of {self.page_size}, "
+                             f"{self.n_kv_heads} heads of {self.head_dim}, not {n_pages} of "
+                             f"{page_size}, {heads} of {dim}")
+
+
+def paged_kv_append_mx4(heads: Heads, q, k, v, q_weight, k_weight, table, positions, slots, q_out,
+                        cache: Mx4Cache, stream=None) -> None:
+    """paged_kv_append into a 4-bit cache: k, normalised and rotated, and v are quantised as
+    they are written."""
+    T, D, dt = heads.T, heads.head_dim, _TORCH_DTYPE[heads.dtype]
+    nq, nk = heads.n_q_heads, heads.n_kv_heads
+    cache._check("paged_kv_append_mx4", cache.n_pages, cache.page_size, nk, D)
+    _check("paged_kv_append_mx4", _lib.paged_kv_append_mx4(
+        heads, *_rows("q", q, T, nq, D, dt), *_rows("k", k, T, nk, D, dt),
+        *_rows("v", v, T, nk, D, dt), *_rotation(heads, q_weight, k_weight, table, positions, dt),
+        _array("slots", slots, T, torch.int32), *_rows("q_out", q_out, T, nq, D, dt), cache._k,
+        cache._v, cache.n_pages, cache.page_size, _stream_ptr(stream, cache.k_codes)))
+
+
+def paged_kv_read_mx4(cache: Mx4Cache, slots, k_out, v_out, stream=None) -> None:
+    """k_out, v_out ([T, n_kv_heads, head_dim] float32 or bfloat16, each may be None): the
+    values of the cache rows `slots` (int32 [T]); those of a slot outside the cache (-1)
+    are left as they were."""
+    out = k_out if k_out is not None else v_out
+    if out is None:
+        return
+    T, nk, D, dt = out.shape[0], cache.n_kv_heads, cache.head_dim, out.dtype
+    _check("paged_kv_read_mx4", _lib.paged_kv_read_mx4(
+        T, nk, D, _code(dt), cache._k, cache._v, cache.n_pages, cache.page_size,
+        _array("slots", slots, T, torch.int32), *_rows("k_out", k_out, T, nk, D, dt),
+        *_rows("v_out", v_out, T, nk, D, dt), _stream_ptr(stream, cache.k_codes)))
+
+
+def paged_attn_mx4_workspace_bytes(batch: PagedBatch) -> int:
+    return int(_lib.paged_attn_mx4_workspace_bytes(batch))
+
+
+def alloc_paged_mx4_workspace(batch: PagedBatch, device=None) -> torch.Tensor:
+    """Device workspace of paged_attn_mx4_fwd (no initial contents needed)."""
+    n = paged_attn_mx4_workspace_bytes(batch)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def paged_attn_mx4_fwd(batch: PagedBatch, q, cache: Mx4Cache, q_start, kv_len, block_table, out,
+                       workspace, lse=None, stream=None) -> None:
+    """paged_attn_fwd over a 4-bit cache."""
+    T, D, dt = batch.T, batch.head_dim, _TORCH_DTYPE[batch.dtype]
+    nq, nk, ns = batch.n_q_heads, batch.n_kv_heads, batch.n_seqs
+    cache._check("paged_attn_mx4_fwd", batch.n_pages, batch.page_size, nk, D)
+    ws, ws_n = (None, 0) if workspace is None else \
+        (_ptr(workspace), workspace.numel() * workspace.element_size())
+    _check("paged_attn_mx4_fwd", _lib.paged_attn_mx4_fwd(
+        batch, *_rows("q", q, T, nq, D, dt), cache._k, cache._v,
+        _array("q_start", q_start, ns + 1, torch.int32), _array("kv_len", kv_len, ns, torch.int32),
+        _table("block_table", block_table, ns, batch.max_pages, torch.int32),
+        *_rows("out", out, T, nq, D, dt), _table("lse", lse, T, nq, torch.float32), ws, ws_n,
+        _stream_ptr(stream, cache.k_codes)))
 
 
 def paged_slots(block_table, seq, positions, page_size: int) -> torch.Tensor:

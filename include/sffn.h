@@ -592,6 +592,77 @@ int32_t paged_attn_fwd(const sffn_paged_batch* batch, const void* q, int64_t q_t
                        float* lse, void* workspace, size_t ws_bytes, void* stream);
 size_t paged_attn_workspace_bytes(const sffn_paged_batch* batch);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The 4-bit paged cache: keys and values as OCP MX FP4, a quarter of bfloat16's bytes
+ * and a scale byte for each 32 elements (head_dim 128: 68 bytes instead of 256).
+ *
+ * A block is up to 32 neighbouring elements of a head (the last one shorter where head_dim
+ * is no multiple of 32).  Its scale byte b stands for 2^(b - 127); 253 to 255 make the whole
+ * block NaN.  An element has four bits, a sign and 0, .5, 1, 1.5, 2, 3, 4 or 6 in
+ * ascending order, times the scale.  A byte of codes holds the element 2 i in its low
+ * four bits and 2 i + 1 in its high ones.  A block with the largest magnitude a is
+ * written with the smallest exponent e in -124 .. 125 for which a < 7 * 2^e (125 where there
+ * is none), elements rounded to the nearest, ties to the even code, larger ones to
+ * 6 * 2^e; a block with an element that is not finite becomes NaN.  Every value that a
+ * block can hold is a bfloat16 number: reading rounds nothing.
+ *
+ * One cache (K or V): codes [n_pages, page_size, n_kv_heads, head_dim / 2] bytes, 4-byte
+ * aligned, the strides of a page, of a token in its page and of a head multiples of 4; scales
+ * [n_pages, page_size, n_kv_heads, ceil(head_dim / 32)] bytes, any strides.  Strides are in
+ * bytes, in any order of these dimensions, the last one contiguous, no two rows
+ * overlapping; that of a dimension of size 1 is not looked at.  A head's tokens of a page
+ * side by side (strides of a head beyond those of a token) is fastest to read: neighbouring
+ * tokens then fill whole cache lines.
+ */
+typedef struct {
+  void* codes;
+  void* scales;
+  int64_t page, token, head;
+  int64_t scale_page, scale_token, scale_head;
+} sffn_mx4;
+
+/*
+ * paged_kv_append_mx4 -- paged_kv_append into a 4-bit cache, one launch: q normalised and
+ * rotated into q_out, k normalised, rotated and quantised into k_cache, v quantised
+ * into v_cache.  The norm and rotation of k are computed in 64 bits and rounded to
+ * float32 before they are quantised, so that what is stored for a token does not depend
+ * on the call that stores it.  Arguments and refusals as for paged_kv_append.
+ */
+int32_t paged_kv_append_mx4(const sffn_heads* heads, const void* q, int64_t q_token, int64_t q_head,
+                            const void* k, int64_t k_token, int64_t k_head, const void* v,
+                            int64_t v_token, int64_t v_head, const void* q_weight,
+                            const void* k_weight, const float* rot_table, const int32_t* positions,
+                            const int32_t* slots, void* q_out, int64_t qo_token, int64_t qo_head,
+                            const sffn_mx4* k_cache, const sffn_mx4* v_cache, int32_t n_pages,
+                            int32_t page_size, void* stream);
+
+/*
+ * paged_kv_read_mx4 -- rows of a 4-bit cache back as values: k_out[t] and v_out[t]
+ * ([T, n_kv_heads, head_dim] dtype, strides as everywhere here) of the cache row slots[t]
+ * (as for the append).  The outputs of a slot outside the cache (-1) are left as they
+ * were.  k_out or v_out may be NULL.  T times n_kv_heads at most 2^27 - 64.
+ */
+int32_t paged_kv_read_mx4(int32_t T, int32_t n_kv_heads, int32_t head_dim, int32_t dtype,
+                          const sffn_mx4* k_cache, const sffn_mx4* v_cache, int32_t n_pages,
+                          int32_t page_size, const int32_t* slots, void* k_out, int64_t ko_token,
+                          int64_t ko_head, void* v_out, int64_t vo_token, int64_t vo_head,
+                          void* stream);
+
+/*
+ * paged_attn_mx4_fwd -- paged_attn_fwd over a 4-bit cache: the same batches, masks,
+ * results, bounds and bits every time, over the values that the cache stands for.  q, out
+ * and the arithmetic are of batch->dtype (float32 or bfloat16).  A NaN block of values that a
+ * row sees makes those elements of its result NaN, one of keys all of them.
+ * workspace: at least paged_attn_mx4_workspace_bytes(batch), no initial contents.
+ */
+int32_t paged_attn_mx4_fwd(const sffn_paged_batch* batch, const void* q, int64_t q_token,
+                           int64_t q_head, const sffn_mx4* k_cache, const sffn_mx4* v_cache,
+                           const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                           void* out, int64_t o_token, int64_t o_head, float* lse, void* workspace,
+                           size_t ws_bytes, void* stream);
+size_t paged_attn_mx4_workspace_bytes(const sffn_paged_batch* batch);
+
 /* Workspace bytes needed by one call for this shape (0 if the shape is invalid). */
 size_t sffn_workspace_bytes(const sffn_shape* shape, int32_t which);
 
