@@ -150,7 +150,9 @@ __device__ __forceinline__ void sequence_range(const AttnArgs& a, KeysWork* k) {
 }
 
 // The items (sequence, tile, split) of attn_keys, numbered through; 64 sequences are
-// held by the lanes of a wave at a time, and the numbers asked for only grow.
+// held by the lanes of a wave at a time, and the numbers asked for only grow.  TM: rows
+// of a tile.
+template <int TM>
 struct KeysItems {
   int s0, base, total;          // first sequence of the 64, items before and in them
   int before, n;                // lane's items before its sequence, and of it
@@ -166,7 +168,7 @@ struct KeysItems {
     if (s < p.n_seqs) bound_sequence(p, p.q_start[s], p.q_start[s + 1], p.kv_len[s], &k.w);
     const int rows = k.w.nq * a.g;
     sequence_range(a, &k);
-    if (rows > 0 && rows <= a.max_rows) n = (rows + 31) / 32 * k.n_split;
+    if (rows > 0 && rows <= a.max_rows) n = (rows + TM - 1) / TM * k.n_split;
     before = prefix_sum(n);
     total = __builtin_amdgcn_readlane(before, kWave - 1);
     before -= n;
@@ -426,7 +428,7 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys(AttnArgs
   // for its place in LDS, so where most are expected to be of that kind (COMPACT:
   // chunks of prompts beside single tokens) only the items that exist are numbered,
   // for 1.5 us to look over the sequences, and a limited grid goes over them.
-  KeysItems items;
+  KeysItems<32> items;
   if constexpr (COMPACT) items.init(a);
   for (int item = blockIdx.x;; item += gridDim.x) {
     KeysWork kw;

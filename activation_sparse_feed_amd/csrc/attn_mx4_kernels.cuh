@@ -25,6 +25,7 @@ namespace sffn {
 struct AttnMx4Args {
   AttnArgs a;
   Mx4Rows k, v;
+  FastDiv heads, tiles;  // key heads; attn_keys_mx4: tiles_per_seq
 };
 
 // Words of codes at p (4-byte aligned); `at`: the element that the first belongs to.
@@ -50,57 +51,93 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, int at, int D, uint
   }
 }
 
-// The scale bytes of the blocks from number b on; 127 (a scale of 1) beyond the head.
+// The scale bytes at p, of the blocks from number b on; 127 (a scale of 1) beyond the head.
 template <int B, bool WHOLE>
 __device__ __forceinline__ void load_scales(const uint8_t* p, int b, int n_blocks, uint32_t (&s)[B]) {
 #pragma unroll
-  for (int i = 0; i < B; ++i) s[i] = WHOLE || b + i < n_blocks ? p[b + i] : 127u;
+  for (int i = 0; i < B; ++i) s[i] = WHOLE || b + i < n_blocks ? p[i] : 127u;
 }
 
 // ------------------------------------------------------------------ many rows
-// Tiles of KT rows of one cache: every thread has PER elements of one row of a tile.  Pages
+// Where a row of codes and its scales lie.
+//   G = 16  page_size is a multiple of 16, and K and V have the same strides, of less than
+//           2^24 bytes for a token and 2^31 for a page: a wave's 16 (or 8) neighbouring rows lie
+//           in one page, which is looked up with scalar instructions, and a lane adds an
+//           offset that never changes.
+//   G = 0   any page size and strides: a lane looks up its own row.  Its 64-bit products
+//           cost more than everything else that a wave does for its keys.
+template <int G>
+struct RowPlace {
+  int page, off;
+
+  // j: the row (G = 0), or the first of the wave's (G = 16).
+  __device__ __forceinline__ void look_up(const int32_t* bt, const FastDiv& per_page, int j, int first, int last) {
+    if constexpr (G > 0) j = min(max(j, first & -G), last & -G);
+    else j = min(max(j, first), last);
+    const int pg = per_page.div(j);
+    off = j - pg * per_page.d;
+    if constexpr (G > 0) page = load_uniform(bt + pg);
+    else page = bt[pg];
+  }
+  // Bytes from the start of the cache to that row.
+  __device__ __forceinline__ int64_t bytes(int last_page, int64_t page_bytes, int64_t token_bytes) const {
+    const uint32_t pg = (uint32_t)min(max(page, 0), last_page);
+    if constexpr (G > 0)
+      return (int64_t)((uint64_t)pg * (uint32_t)page_bytes + (uint64_t)(uint32_t)off * (uint32_t)token_bytes);
+    else return (int64_t)pg * page_bytes + off * token_bytes;
+  }
+};
+
+// Tiles of KT rows of one cache: every thread has kPer elements of one row of a tile.  Pages
 // are looked up two tiles ahead, codes loaded one ahead, and turned into values in LDS
 // in the layout of AttnTile (elements from head_dim to the end of an LDS row: 0).
-template <typename T, int DP, int KT, int NT, bool K>
+template <typename T, int DP, int KT, int NT, int G, bool K>
 struct Mx4Loader {
   typedef AttnTile<T, DP, KT> Tile;
   static constexpr int kPer = KT * Tile::kRowElems / NT;
   static constexpr int kParts = Tile::kRowElems / kPer;  // threads of a row
   static constexpr int kW = kPer / 8;
   static constexpr int kB = kPer < kMxBlock ? 1 : kPer / kMxBlock;
-  static_assert(kPer % 8 == 0 && kPer * kParts == Tile::kRowElems, "");
+  static_assert(kPer % 8 == 0 && kPer * kParts == Tile::kRowElems && kWave / kParts <= 16, "");
   const int32_t* bt;
-  const uint8_t *codes, *scales;  // of the key head, at this thread's elements
+  const uint8_t *codes, *scales;  // of the key head
   int64_t page_bytes, token_bytes, s_page, s_token;
+  uint32_t lane_codes, lane_scales;  // G > 0: this lane's row, from the wave's first
   FastDiv per_page;
   int last_page, first, last, row, part, D;
-  int page, off;
+  RowPlace<G> at;
   uint32_t w[kW], s[kB];
 
   __device__ __forceinline__ void init(const AttnArgs& a, const Mx4Rows& c, int seq, int hk, int lo, int hi) {
     row = (int)threadIdx.x / kParts, part = (int)threadIdx.x % kParts;
     bt = a.p.block_table + (size_t)seq * a.p.max_pages;
-    codes = c.codes + hk * c.head + part * (kPer / 2);
+    codes = c.codes + hk * c.head;
     scales = c.scales + hk * c.s_head;
     page_bytes = c.page, token_bytes = c.token, s_page = c.s_page, s_token = c.s_token;
+    const int r = G > 0 ? lane_id() / kParts : 0;
+    lane_codes = (uint32_t)r * (uint32_t)c.token + part * (kPer / 2);
+    lane_scales = (uint32_t)r * (uint32_t)c.s_token + part * kPer / kMxBlock;
     per_page = a.page;
     last_page = a.p.n_pages - 1;
     first = lo, last = hi - 1;
     D = a.p.D;
   }
+  // A wave of eight rows looks up the sixteen around them.
   __device__ __forceinline__ void look_up(int j0) {
-    const int j = min(max(j0 + row, first), last);
-    const int pg = per_page.div(j);
-    off = j - pg * per_page.d;
-    page = bt[pg];
+    if constexpr (G > 0) {
+      constexpr int kRows = kWave / kParts;
+      at.look_up(bt, per_page, j0 + uniform(row) / 16 * 16, first, last);
+      if constexpr (kRows < 16) at.off += uniform(row) % 16;
+    } else {
+      at.look_up(bt, per_page, j0 + row, first, last);
+    }
   }
   __device__ __forceinline__ void start() {
-    const int64_t pg = min(max(page, 0), last_page);
-    const uint8_t* c = codes + pg * page_bytes + off * token_bytes;
-    const uint8_t* b = scales + pg * s_page + off * s_token;
+    const uint8_t* c = codes + at.bytes(last_page, page_bytes, token_bytes) + lane_codes;
+    const uint8_t* b = scales + at.bytes(last_page, s_page, s_token) + lane_scales;
     if (D == Tile::kRowElems) {
       load_codes<kW, true>(c, 0, D, w);
-      load_scales<kB, true>(b, part * kPer / kMxBlock, 0, s);
+      load_scales<kB, true>(b, 0, 0, s);
     } else {
       load_codes<kW, false>(c, part * kPer, D, w);
       load_scales<kB, false>(b, part * kPer / kMxBlock, mx_blocks(D), s);
@@ -121,7 +158,7 @@ struct Mx4Loader {
   }
 };
 
-template <typename T, int DP, int KT, int NW>
+template <typename T, int DP, int KT, int NW, int G>
 __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 && NW == 4 ? 2 : 1) void attn_rows_mx4(
     AttnMx4Args m) {
   typedef AttnTile<T, DP, KT> Tile;
@@ -141,8 +178,8 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 && NW == 4 ? 2
   const int b = pl.b, e = pl.e, x = pl.x, y = pl.y;
   Tile tile;
   tile.init();
-  Mx4Loader<T, DP, KT, NW * 64, true> load_k;
-  Mx4Loader<T, DP, KT, NW * 64, false> load_v;
+  Mx4Loader<T, DP, KT, NW * 64, G, true> load_k;
+  Mx4Loader<T, DP, KT, NW * 64, G, false> load_v;
   load_k.init(a, m.k, pl.w.seq, hk, b, e);
   load_v.init(a, m.v, pl.w.seq, hk, b, e);
   // as in attn_rows the K tile beside a V tile is 32 keys ahead of it
@@ -273,25 +310,40 @@ struct KeysTile {
       l[t] = 0.f;
     }
   }
-  __device__ __forceinline__ void load_q(int t, const T* row, int D, bool negate) {
+  // Loads without conditions, so that they are in flight together; finish_q once they are
+  // all under way.
+  template <bool WHOLE>
+  __device__ __forceinline__ void load_q(int t, const T* row, int D) {
     const int e0 = (lane_id() >> 4) * kLane;
 #pragma unroll
     for (int i = 0; i < kW * kC; ++i) {
       const int e = e0 + i * kEpc;
-      q[t][i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (e < D) q[t][i] = ldg16(row + e);
+      q[t][i] = ldg16(row + (WHOLE ? e : min(e, D - kEpc)));
     }
-    if (negate)
+  }
+  template <bool WHOLE>
+  __device__ __forceinline__ void finish_q(int t, int D, bool negate) {
+    const int e0 = (lane_id() >> 4) * kLane;
+    const uint32_t sign = negate ? (sizeof(T) == 2 ? 0x80008000u : 0x80000000u) : 0u;
 #pragma unroll
-      for (int i = 0; i < kW * kC; ++i) q[t][i] = Frag<T>::negate(q[t][i]);
+    for (int i = 0; i < kW * kC; ++i) {
+      if (!WHOLE && e0 + i * kEpc >= D) q[t][i] = u32x4_t{0u, 0u, 0u, 0u};
+      q[t][i] ^= sign;
+    }
   }
 
   // Codes and scales of one row of K or V, this lane's part.
   struct Codes {
     uint32_t w[kW], s[kB];
   };
-  static __device__ __forceinline__ float scale_of(const Codes& c, int i) {
+  // Word i's scale.  A NaN block of V counts as (about) 0 here: 0 times NaN would be NaN for
+  // the rows that do not see it.  The rows that do get their NaN at the end.
+  static __device__ __forceinline__ float scale_k(const Codes& c, int i) {
     return mx_scale(c.s[i / 4 < kB ? i / 4 : 0]);
+  }
+  static __device__ __forceinline__ float scale_v(const Codes& c, int i) {
+    const uint32_t s = c.s[i / 4 < kB ? i / 4 : 0];
+    return __uint_as_float((s >= kMxBad ? 0u : s) << 23);
   }
 
   // Scores of 16 keys: s[t] has the keys 4 (lane / 16) + i of row lane % 16.
@@ -301,7 +353,7 @@ struct KeysTile {
 #pragma unroll
     for (int i = 0; i < kW; ++i) {
       u32x4_t x[kC];
-      Mx<T>::decode8(k.w[i], scale_of(k, i), x);
+      Mx<T>::decode8(k.w[i], scale_k(k, i), x);
 #pragma unroll
       for (int j = 0; j < kC; ++j)
 #pragma unroll
@@ -315,7 +367,7 @@ struct KeysTile {
 #pragma unroll
     for (int i = 0; i < kW; ++i) {
       u32x4_t x[kC];
-      Mx<T>::decode8(v.w[i], scale_of(v, i), x);
+      Mx<T>::decode8(v.w[i], scale_v(v, i), x);
 #pragma unroll
       for (int j = 0; j < kC; ++j)
         *(u32x4_t*)(lds + r * kPitch + (((c0 + i * kC + j) ^ swz(r)) << 4)) = x[j];
@@ -386,56 +438,29 @@ struct KeysTile {
       l[t] += s[i];
     }
   }
-
-  // A NaN block of V in a tile with hidden keys: rows that see its key get NaN in its
-  // elements, and it becomes 0 for the others (0 times NaN is NaN).  j: this lane's
-  // key, jb: the block's first.
-  __device__ __forceinline__ void take_nan(Codes& v, int jb, const int (&lo)[RT], const int (&hi)[RT]) {
-#pragma unroll
-    for (int n = 0; n < kB; ++n) {
-      uint64_t bad = __ballot(v.s[n] >= kMxBad);
-      if (bad == 0) continue;
-      while (bad != 0) {
-        const int at = (int)__builtin_ctzll(bad);
-        bad &= bad - 1;
-        const int j = jb + (at & 15), e0 = (at >> 4) * kLane + n * kMxBlock;
-        const int e1 = e0 + (kLane < kMxBlock ? kLane : kMxBlock);
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-          if (j >= lo[t] && j < hi[t]) {
-#pragma unroll
-            for (int d = 0; d < kDt; ++d)
-              if (d * 16 >= e0 && d * 16 < e1)
-                o[t][d] = f32x4_t{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
-          }
-      }
-      if (v.s[n] >= kMxBad) {
-        v.s[n] = 0;
-#pragma unroll
-        for (int i = 0; i < kW; ++i)
-          if ((i / 4 < kB ? i / 4 : 0) == n) v.w[i] = 0;
-      }
-    }
-  }
 };
 
 // The rows of K and V of a wave's blocks of 32 keys: lane l has key l % 16 of both halves.
 // Pages are looked up one block before codes are loaded.
-template <typename T, int DP, int RT, bool WHOLE>
+template <typename T, int DP, int RT, int G, bool WHOLE>
 struct KeysLoader {
   typedef KeysTile<T, DP, RT> Tile;
   const int32_t* bt;
-  Mx4Rows k, v;                  // of the key head, at this lane's elements
+  Mx4Rows k, v;                  // of the key head
+  uint32_t k_lane, v_lane, ks_lane, vs_lane;  // this lane's bytes from the row that was looked up
   FastDiv per_page;
-  int last_page, first, last, D, at;
-  int page[2], off[2];
+  int last_page, first, last, D, e0;
+  RowPlace<G> at[2];
 
   __device__ __forceinline__ void init(const AttnMx4Args& m, int seq, int hk, int lo, int hi) {
-    at = (lane_id() >> 4) * Tile::kLane;
+    e0 = (lane_id() >> 4) * Tile::kLane;
     bt = m.a.p.block_table + (size_t)seq * m.a.p.max_pages;
     k = m.k, v = m.v;
-    k.codes += hk * k.head + at / 2, k.scales += hk * k.s_head;
-    v.codes += hk * v.head + at / 2, v.scales += hk * v.s_head;
+    k.codes += hk * k.head, k.scales += hk * k.s_head;
+    v.codes += hk * v.head, v.scales += hk * v.s_head;
+    const uint32_t r = G > 0 ? lane_id() & 15 : 0;
+    k_lane = r * (uint32_t)k.token + e0 / 2, ks_lane = r * (uint32_t)k.s_token + e0 / kMxBlock;
+    v_lane = r * (uint32_t)v.token + e0 / 2, vs_lane = r * (uint32_t)v.s_token + e0 / kMxBlock;
     per_page = m.a.page;
     last_page = m.a.p.n_pages - 1;
     first = lo, last = hi - 1;
@@ -443,30 +468,77 @@ struct KeysLoader {
   }
   __device__ __forceinline__ void look_up(int j0) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int j = min(max(j0 + 16 * b + (lane_id() & 15), first), last);
-      const int pg = per_page.div(j);
-      off[b] = j - pg * per_page.d;
-      page[b] = bt[pg];
-    }
+    for (int b = 0; b < 2; ++b)
+      at[b].look_up(bt, per_page, j0 + 16 * b + (G > 0 ? 0 : lane_id() & 15), first, last);
   }
-  __device__ __forceinline__ void one(const Mx4Rows& c, int64_t pg, int b, typename Tile::Codes& x) const {
-    load_codes<Tile::kW, WHOLE>(c.codes + pg * c.page + off[b] * c.token, at, D, x.w);
-    load_scales<Tile::kB, WHOLE>(c.scales + pg * c.s_page + off[b] * c.s_token, at / kMxBlock,
-                                 mx_blocks(D), x.s);
+  __device__ __forceinline__ void one(const uint8_t* codes, const uint8_t* scales,
+                                      typename Tile::Codes& x) const {
+    load_codes<Tile::kW, WHOLE>(codes, e0, D, x.w);
+    load_scales<Tile::kB, WHOLE>(scales, e0 / kMxBlock, mx_blocks(D), x.s);
   }
   __device__ __forceinline__ void start(typename Tile::Codes (&kc)[2], typename Tile::Codes (&vc)[2]) const {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const int64_t pg = min(max(page[b], 0), last_page);
-      one(k, pg, b, kc[b]);
-      one(v, pg, b, vc[b]);
+      one(k.codes + at[b].bytes(last_page, k.page, k.token) + k_lane,
+          k.scales + at[b].bytes(last_page, k.s_page, k.s_token) + ks_lane, kc[b]);
+      one(v.codes + at[b].bytes(last_page, v.page, v.token) + v_lane,
+          v.scales + at[b].bytes(last_page, v.s_page, v.s_token) + vs_lane, vc[b]);
     }
   }
 };
 
-template <typename T, int DP, int RT, int NW, bool WHOLE, bool COMPACT>
-__global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys_mx4(AttnMx4Args args) {
+// Rows of an attn_keys_mx4 tile: two tiles of 16 share what is decoded where the registers
+// hold their outputs.
+constexpr int keys_mx4_rows(int elt_bytes, int head_dim, int64_t rows) {
+  return rows > 16 && elt_bytes == 2 && head_dim <= 128 ? 32 : 16;
+}
+// Waves of a workgroup.
+#ifndef SFFN_NW
+#define SFFN_NW 8
+#endif
+constexpr int keys_mx4_waves(int elt_bytes, int head_dim) {
+  return elt_bytes == 4 && head_dim > 128 ? 4 : SFFN_NW;
+}
+// Waves of a SIMD that the registers are meant for.
+constexpr int keys_mx4_occupancy(int elt_bytes, int dp, int row_tiles, bool compact) {
+  if (elt_bytes == 4) return dp > 128 ? 1 : 2;
+  if (dp > 128) return compact ? 1 : 2;
+  return row_tiles == 2 ? 2 : compact ? 3 : 4;
+}
+
+// The wave's keys once more, where one of them had a NaN block of V: rows that see its key
+// get NaN in the block's elements.  Out of the way of the loop: on the rows that the wave has
+// left in LDS, by lane.
+template <typename T, int DP, int RT, int G, typename Loader>
+__device__ __forceinline__ void mark_nan(const AttnMx4Args& m, Loader& load, const Work& w, int hk, int r0, int rows,
+                                      int j0, int end, int step, uint8_t* lds) {
+  const AttnArgs& a = m.a;
+  const int lane = lane_id(), n_blocks = mx_blocks(a.p.D);
+  for (; j0 < end; j0 += step) {
+    load.look_up(j0);
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* row = load.v.scales + load.at[h].bytes(load.last_page, load.v.s_page, load.v.s_token) +
+                           (G > 0 ? (int64_t)(lane & 15) * load.v.s_token : 0);
+      for (int n = 0; n < n_blocks; ++n) {
+        uint64_t bad = __ballot(lane < 16 && row[n] >= kMxBad);
+        while (bad != 0) {
+          const int j = j0 + 16 * h + (int)__builtin_ctzll(bad);
+          bad &= bad - 1;
+          for (int r = 0; r < rows; ++r) {
+            int lo, hi;
+            key_range(a.p, w, a.group.div(r0 + r), &lo, &hi);
+            const int e = n * kMxBlock + lane;
+            if (j >= lo && j < hi && lane < kMxBlock && e < a.p.D)
+              *(float*)(lds + r * (DP * 4) + (((e / 4) ^ (r & 7)) << 4) + (e & 3) * 4) = __builtin_nanf("");
+          }
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int DP, int RT, int NW, int G, bool WHOLE, bool COMPACT>
+__global__ __launch_bounds__(NW * 64, keys_mx4_occupancy(sizeof(T), DP, RT, COMPACT)) void attn_keys_mx4(AttnMx4Args args) {
   typedef KeysTile<T, DP, RT> Tile;
   constexpr int TM = 16 * RT;
   __shared__ __align__(1024) uint8_t lds[NW][Tile::kLdsBytes];
@@ -476,16 +548,16 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys_mx4(Attn
   const int wave = uniform((int)threadIdx.x / kWave), lane = lane_id(), quad = lane >> 4;
   uint8_t* const mine = lds[wave];
   // items as in attn_keys
-  KeysItems items;
+  KeysItems<TM> items;
   if constexpr (COMPACT) items.init(a);
   for (int item = blockIdx.x;; item += gridDim.x) {
     KeysWork kw;
-    const int hk = item % p.hkv;
+    const int hk = item - args.heads.div(item) * p.hkv;
     if constexpr (COMPACT) {
-      if (!items.get(a, item / p.hkv, &kw)) break;
+      if (!items.get(a, args.heads.div(item), &kw)) break;
     } else {
       kw.split = blockIdx.y;
-      const int t = item / p.hkv, s = t / a.tiles_per_seq;
+      const int t = args.heads.div(item), s = args.tiles.div(t);
       read_sequence(p, s, &kw.w);
       kw.w.tile = t - s * a.tiles_per_seq;
       const int all = kw.w.nq * a.g;
@@ -504,37 +576,38 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys_mx4(Attn
     int row_lo[RT], row_hi[RT];
     Tile tile;
     tile.init();
-    KeysLoader<T, DP, RT, WHOLE> load;
+    KeysLoader<T, DP, RT, G, WHOLE> load;
     load.init(args, w.seq, hk, b, e);
     int j0 = (b & ~31) + wave * 32;
     const int end = b < e ? e : j0, step = NW * 32;
-    typename Tile::Codes ka[2], va[2], kb[2], vb[2];
+    typename Tile::Codes kc[2], vc[2];
+    uint32_t worst = 0;  // scale byte of V
     if (j0 < end) {
       load.look_up(j0);
-      load.start(ka, va);
+      load.start(kc, vc);
       load.look_up(j0 + step);
-      if (j0 + step < end) load.start(kb, vb);
-      load.look_up(j0 + 2 * step);
     }
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const int r = r0 + min(16 * t + (lane & 15), rows - 1);
       const int token = a.group.div(r), head = hk * a.g + r - token * a.g;
       key_range(p, w, token, &row_lo[t], &row_hi[t]);
-      if (j0 < end)
-        tile.load_q(t, (const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D, a.negate);
+      tile.template load_q<WHOLE>(t, (const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D);
     }
-    // One block of 32 keys, whose codes have been on their way for two of the wave's
-    // blocks; those of the block after the next take their place.
-    auto block = [&](typename Tile::Codes (&kc)[2], typename Tile::Codes (&vc)[2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) tile.template finish_q<WHOLE>(t, p.D, a.negate);
+    // Blocks of 32 keys.  Once a block's codes have become operands those of the next are
+    // loaded in their place: with four waves a SIMD that is enough under way (with a second
+    // set of registers and three waves: decode of 32 tokens 25.0 us instead of 23.1, of three
+    // long sequences 69.2 instead of 59.4).
+    for (; j0 < end; j0 += step) {
       const bool whole = j0 >= x && j0 + 32 <= y;
       f32x4_t s[2][RT];
 #pragma unroll
       for (int h = 0; h < 2; ++h) tile.scores(kc[h], s[h]);
       if (!whole) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          tile.take_nan(vc[h], j0 + 16 * h, row_lo, row_hi);
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -542,13 +615,16 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys_mx4(Attn
               const int j = j0 + 16 * h + 4 * quad + i;
               s[h][t][i] = j >= row_lo[t] && j < row_hi[t] ? s[h][t][i] : -INFINITY;
             }
-        }
       }
 #pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < Tile::kB; ++n) worst = max(worst, vc[h].s[n]);
+#pragma unroll
       for (int h = 0; h < 2; ++h) Tile::write_v(mine, h, vc[h]);
-      if (j0 + 2 * step < end) {
+      if (j0 + step < end) {
         load.start(kc, vc);
-        load.look_up(j0 + 3 * step);
+        load.look_up(j0 + 2 * step);
       }
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
@@ -559,12 +635,6 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys_mx4(Attn
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       tile.accumulate(mine, s);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      j0 += step;
-    };
-    while (j0 < end) {
-      block(ka, va);
-      if (j0 >= end) break;
-      block(kb, vb);
     }
     // Join the waves: each leaves its rows in its LDS, row r's 16-byte chunk c at c ^ (r % 8).
 #pragma unroll
@@ -578,6 +648,10 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys_mx4(Attn
         ml[wave][row][0] = tile.m[t] * a.c;
         ml[wave][row][1] = l;
       }
+    }
+    if (__any(worst >= kMxBad)) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      mark_nan<T, DP, RT, G>(args, load, w, hk, r0, rows, (b & ~31) + wave * 32, end, step, mine);
     }
     __syncthreads();
     const int quads = p.D / 4;
@@ -614,39 +688,46 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys_mx4(Attn
   }
 }
 
-constexpr int kMx4KeysWaves = 4;
-
-// Launches of one element type, in files of their own.
-template <typename T> hipError_t launch_attn_rows_mx4(const AttnMx4Args& m, hipStream_t s);
-template <typename T> hipError_t launch_attn_keys_mx4(const AttnMx4Args& m, int row_tiles, bool compact, hipStream_t s);
+// Launches of one element type, in files of their own.  near: rows can be looked up by 16.
+template <typename T> hipError_t launch_attn_rows_mx4(const AttnMx4Args& m, bool near, hipStream_t s);
+template <typename T>
+hipError_t launch_attn_keys_mx4(const AttnMx4Args& m, int tile_rows, bool near, bool compact, hipStream_t s);
 
 template <typename T, int DP>
-hipError_t attn_rows_mx4_width(const AttnMx4Args& m, hipStream_t s) {
+hipError_t attn_rows_mx4_width(const AttnMx4Args& m, bool near, hipStream_t s) {
   constexpr int kKeys = RowsShape<T, DP>::kKeys, kWaves = RowsShape<T, DP>::kWaves;
   const AttnArgs& a = m.a;
   const dim3 grid((unsigned)(a.n_tiles * a.p.hkv), (unsigned)a.splits), block(kWaves * 64);
-  hipLaunchKernelGGL((attn_rows_mx4<T, DP, kKeys, kWaves>), grid, block, 0, s, m);
+  if (near) hipLaunchKernelGGL((attn_rows_mx4<T, DP, kKeys, kWaves, 16>), grid, block, 0, s, m);
+  else hipLaunchKernelGGL((attn_rows_mx4<T, DP, kKeys, kWaves, 0>), grid, block, 0, s, m);
   return hipGetLastError();
 }
 
-template <typename T, int DP, int RT, bool WHOLE>
+template <typename T, int DP, int RT, int G, bool WHOLE>
 hipError_t attn_keys_mx4_go(const AttnMx4Args& m, bool compact, hipStream_t s) {
+  constexpr int kWaves = keys_mx4_waves(sizeof(T), DP);
   const AttnArgs& a = m.a;
   const int64_t items = (int64_t)a.n_tiles * a.p.hkv * a.splits, most = 2 * kCus;
   const dim3 all((unsigned)(a.n_tiles * a.p.hkv), (unsigned)a.splits);
-  const dim3 some((unsigned)(items < most ? items : most)), block(kMx4KeysWaves * 64);
-  if (compact) hipLaunchKernelGGL((attn_keys_mx4<T, DP, RT, kMx4KeysWaves, WHOLE, true>), some, block, 0, s, m);
-  else hipLaunchKernelGGL((attn_keys_mx4<T, DP, RT, kMx4KeysWaves, WHOLE, false>), all, block, 0, s, m);
+  const dim3 some((unsigned)(items < most ? items : most)), block(kWaves * 64);
+  if (compact) hipLaunchKernelGGL((attn_keys_mx4<T, DP, RT, kWaves, G, WHOLE, true>), some, block, 0, s, m);
+  else hipLaunchKernelGGL((attn_keys_mx4<T, DP, RT, kWaves, G, WHOLE, false>), all, block, 0, s, m);
   return hipGetLastError();
 }
 
+template <typename T, int DP, int RT>
+hipError_t attn_keys_mx4_rows(const AttnMx4Args& m, bool near, bool compact, hipStream_t s) {
+  if (!near) return attn_keys_mx4_go<T, DP, RT, 0, false>(m, compact, s);
+  return m.a.p.D == DP ? attn_keys_mx4_go<T, DP, RT, 16, true>(m, compact, s)
+                       : attn_keys_mx4_go<T, DP, RT, 16, false>(m, compact, s);
+}
+
+// tile_rows: of keys_mx4_rows.
 template <typename T, int DP>
-hipError_t attn_keys_mx4_width(const AttnMx4Args& m, int row_tiles, bool compact, hipStream_t s) {
-  if (m.a.p.D == DP)
-    return row_tiles == 1 ? attn_keys_mx4_go<T, DP, 1, true>(m, compact, s)
-                          : attn_keys_mx4_go<T, DP, 2, true>(m, compact, s);
-  return row_tiles == 1 ? attn_keys_mx4_go<T, DP, 1, false>(m, compact, s)
-                        : attn_keys_mx4_go<T, DP, 2, false>(m, compact, s);
+hipError_t attn_keys_mx4_width(const AttnMx4Args& m, int tile_rows, bool near, bool compact, hipStream_t s) {
+  if constexpr (keys_mx4_rows(sizeof(T), DP, 32) == 32)
+    if (tile_rows == 32) return attn_keys_mx4_rows<T, DP, 2>(m, near, compact, s);
+  return attn_keys_mx4_rows<T, DP, 1>(m, near, compact, s);
 }
 
 }  // namespace sffn

@@ -4,9 +4,9 @@
 namespace sffn {
 
 template <>
-hipError_t launch_attn_rows_mx4<float>(const AttnMx4Args& m, hipStream_t s) {
+hipError_t launch_attn_rows_mx4<float>(const AttnMx4Args& m, bool near, hipStream_t s) {
   const AttnArgs& a = m.a;
-  SFFN_ATTN_BY_WIDTH(attn_rows_mx4_width, float, m, s);
+  SFFN_ATTN_BY_WIDTH(attn_rows_mx4_width, float, m, near, s);
 }
 
 }  // namespace sffn

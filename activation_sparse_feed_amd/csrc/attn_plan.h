@@ -72,6 +72,7 @@ inline void split(Plan* pl, const PagedAttn& p, int64_t span, int64_t groups, in
 // Key ranges of up to `whole` keys are not split, longer ones into chunks of least .. most.
 struct KeysTuning {
   int whole, least, most, want;  // want: workgroups
+  int tile;                      // rows of one
 };
 
 inline Plan plan_keys(const PagedAttn& p, const KeysTuning& n) {
@@ -84,7 +85,7 @@ inline Plan plan_keys(const PagedAttn& p, const KeysTuning& n) {
   pl.used = g <= limit && (rows <= limit || !equal);
   if (!pl.used) return pl;
   pl.max_rows = limit;
-  pl.tiles_per_seq = (int)(((rows < limit ? rows : limit) + kKeysTile - 1) / kKeysTile);
+  pl.tiles_per_seq = (int)(((rows < limit ? rows : limit) + n.tile - 1) / n.tile);
   pl.tiles = p.n_seqs * pl.tiles_per_seq;
   pl.slot_rows = (int)(rows < limit ? rows : limit);
   pl.part_rows = (size_t)p.n_seqs * p.hkv * pl.slot_rows;
@@ -164,14 +165,16 @@ inline AttnArgs attn_args(const PagedAttn& p) {
 // attn_join for the rows of kRowsTile or kKeysTile.
 hipError_t launch_attn_join(int dtype, int tile_rows, const AttnArgs& a, dim3 grid, hipStream_t s);
 
-// The join of the splits of one of the two kernels, where there are any.
-inline hipError_t launch_join(int dtype, int tile_rows, const AttnArgs& a, const Plan& pl, hipStream_t s) {
+// The join of the splits of one of the two kernels, where there are any.  Rows of attn_keys
+// are joined by 32, whatever its tiles.
+inline hipError_t launch_join(int dtype, int tile_rows, AttnArgs a, const Plan& pl, hipStream_t s) {
   if (pl.splits <= 1) return hipSuccess;
   const PagedAttn& p = a.p;
-  const int all = (int)((int64_t)p.max_q * a.g < kKeysTile ? p.max_q * a.g : kKeysTile);
-  const dim3 grid = tile_rows == kKeysTile ? join_grid(pl.tiles * p.hkv, all, 4096)
-                                           : join_grid(pl.tiles * p.hkv, tile_rows / 4, 1024);
-  return launch_attn_join(dtype, tile_rows, a, grid, s);
+  if (tile_rows != kKeysTile)
+    return launch_attn_join(dtype, tile_rows, a, join_grid(pl.tiles * p.hkv, tile_rows / 4, 1024), s);
+  a.tiles_per_seq = (pl.slot_rows + kKeysTile - 1) / kKeysTile;
+  const int rows = pl.slot_rows < kKeysTile ? pl.slot_rows : kKeysTile;
+  return launch_attn_join(dtype, tile_rows, a, join_grid(p.n_seqs * a.tiles_per_seq * p.hkv, rows, 4096), s);
 }
 
 }  // namespace sffn

@@ -195,7 +195,8 @@ constexpr int kHeadsBlock = 256;
 
 // Part `part` of a token's heads, by one wave: the rows of q, then of k, then (to
 // a cache) of v, 64 / G at a time.
-template <typename T, int V>
+// Q: of q alone.
+template <typename T, int V, bool Q = false>
 __device__ __forceinline__ void heads_fwd_part(const HeadsFwd& p, int t, int part) {
   const int lane = lane_id();
   const int G = p.lanes_per_row, u = lane & (G - 1), sub = lane / G, rpw = kWave / G;
@@ -203,7 +204,7 @@ __device__ __forceinline__ void heads_fwd_part(const HeadsFwd& p, int t, int par
   const Unit un = unit_of<V>(u, p.D, p.rot, adjacent);
   int64_t kc = (int64_t)t * p.ko_token, vc = 0;
   bool stored = true;
-  if (p.slots != nullptr) {
+  if (!Q && p.slots != nullptr) {
     const int slot = p.slots[t];
     stored = slot >= 0 && (int64_t)slot < (int64_t)p.n_pages * p.page_size;
     const int page = stored ? slot / p.page_size : 0, off = stored ? slot % p.page_size : 0;
@@ -215,16 +216,16 @@ __device__ __forceinline__ void heads_fwd_part(const HeadsFwd& p, int t, int par
   RawWeight<T, V> wq, wk;
   if (p.norm) {
     wq.load((const T*)p.q_weight, un);
-    wk.load((const T*)p.k_weight, un);
+    if (!Q) wk.load((const T*)p.k_weight, un);
   }
   const int n_v = p.slots != nullptr ? p.hkv : 0;
-  const int rows = p.hq + p.hkv + n_v;
+  const int rows = Q ? p.hq : p.hq + p.hkv + n_v;
   const float inv_d = 1.f / (float)p.D;
   for (int r0 = part * p.rows_per_wave; r0 < min(rows, (part + 1) * p.rows_per_wave);
        r0 += rpw) {
     const int r = r0 + sub;
     const bool in = r < rows;
-    const bool is_q = r < p.hq, is_k = !is_q && r < p.hq + p.hkv;
+    const bool is_q = Q || r < p.hq, is_k = !is_q && r < p.hq + p.hkv;
     const int h = is_q ? r : is_k ? r - p.hq : r - p.hq - p.hkv;
     const T* src = is_q ? (const T*)p.q + t * p.q_token + h * p.q_head
                  : is_k ? (const T*)p.k + t * p.k_token + h * p.k_head

@@ -20,8 +20,8 @@ namespace {
 // fewer spread a few long ranges over the GPU.
 Plan keys_of(int dtype, const PagedAttn& p) {
   const int step = attn_keys_waves(dtype == 1 ? 2 : 4, p.D) * 32;
-  return plan_keys(p, dtype == 1 ? KeysTuning{step * 5, step * 2, step * 6, 4 * kCus}
-                                 : KeysTuning{step * 2, step, step, 4 * kCus});
+  return plan_keys(p, dtype == 1 ? KeysTuning{step * 5, step * 2, step * 6, 4 * kCus, kKeysTile}
+                                 : KeysTuning{step * 2, step, step, 4 * kCus, kKeysTile});
 }
 Plan rows_of(int dtype, const PagedAttn& p, const Plan& keys) {
   return plan_rows(p, keys.used, dtype == 1 ? 256 : 128);

@@ -7,17 +7,20 @@
 
 namespace sffn {
 
-template <> hipError_t launch_attn_rows_mx4<uint16_t>(const AttnMx4Args&, hipStream_t);
-template <> hipError_t launch_attn_rows_mx4<float>(const AttnMx4Args&, hipStream_t);
-template <> hipError_t launch_attn_keys_mx4<uint16_t>(const AttnMx4Args&, int, bool, hipStream_t);
-template <> hipError_t launch_attn_keys_mx4<float>(const AttnMx4Args&, int, bool, hipStream_t);
+template <> hipError_t launch_attn_rows_mx4<uint16_t>(const AttnMx4Args&, bool, hipStream_t);
+template <> hipError_t launch_attn_rows_mx4<float>(const AttnMx4Args&, bool, hipStream_t);
+template <> hipError_t launch_attn_keys_mx4<uint16_t>(const AttnMx4Args&, int, bool, bool, hipStream_t);
+template <> hipError_t launch_attn_keys_mx4<float>(const AttnMx4Args&, int, bool, bool, hipStream_t);
 
 namespace {
 
+int tile_of(int dtype, const PagedAttn& p) {
+  return keys_mx4_rows(dtype == 1 ? 2 : 4, p.D, p.max_q * (int64_t)(p.hq / p.hkv));
+}
 Plan keys_of(int dtype, const PagedAttn& p) {
-  const int step = kMx4KeysWaves * 32;
-  return plan_keys(p, dtype == 1 ? KeysTuning{step * 5, step * 2, step * 6, 4 * kCus}
-                                 : KeysTuning{step * 2, step, step, 4 * kCus});
+  const int step = keys_mx4_waves(dtype == 1 ? 2 : 4, p.D) * 32, tile = tile_of(dtype, p);
+  return plan_keys(p, dtype == 1 ? KeysTuning{step * 5, step * 2, step * 6, 4 * kCus, tile}
+                                 : KeysTuning{step * 2, step, step, 4 * kCus, tile});
 }
 Plan rows_of(int dtype, const PagedAttn& p, const Plan& keys) {
   return plan_rows(p, keys.used, dtype == 1 ? 256 : 128);
@@ -27,18 +30,22 @@ template <typename T>
 hipError_t launch(AttnMx4Args m, const Plan& keys, const Plan& rows, void* ws, hipStream_t s) {
   AttnArgs& a = m.a;
   const int dtype = sizeof(T) == 2 ? 1 : 0;
+  // see RowPlace
+  const Mx4Rows &k = m.k, &v = m.v;
+  const bool alike = k.page == v.page && k.token == v.token && k.s_page == v.s_page && k.s_token == v.s_token;
+  const bool small = k.token < (1 << 24) && k.s_token < (1 << 24) && k.page < (1ll << 31) && k.s_page < (1ll << 31);
+  const bool near = a.p.page_size % 16 == 0 && alike && small;
   hipError_t e = hipSuccess;
   if (rows.used) {
     place(&a, rows, (char*)ws + keys.bytes);
-    e = launch_attn_rows_mx4<T>(m, s);
+    e = launch_attn_rows_mx4<T>(m, near, s);
     if (e == hipSuccess) e = launch_join(dtype, kRowsTile, a, rows, s);
     if (e != hipSuccess) return e;
   }
   if (keys.used) {
     place(&a, keys, ws);
-    // one tile of 16 rows where no sequence that the kernel takes has more
-    const int row_tiles = (int64_t)a.p.max_q * a.g <= 16 ? 1 : 2;
-    e = launch_attn_keys_mx4<T>(m, row_tiles, rows.used, s);
+    m.tiles = FastDiv::make(a.tiles_per_seq);
+    e = launch_attn_keys_mx4<T>(m, tile_of(dtype, a.p), near, rows.used, s);
     if (e == hipSuccess) e = launch_join(dtype, kKeysTile, a, keys, s);
   }
   return e;
@@ -50,7 +57,7 @@ bool plan_paged_attn_mx4(int dtype, const PagedAttn& p, size_t* bytes) {
   *bytes = 0;
   if (p.T == 0 || p.n_seqs == 0 || p.max_q == 0) return true;  // nothing is launched
   const Plan keys = keys_of(dtype, p), rows = rows_of(dtype, p, keys);
-  if (!plan_fits(keys, rows, p, kMx4KeysWaves * kWave)) return false;
+  if (!plan_fits(keys, rows, p, keys_mx4_waves(dtype == 1 ? 2 : 4, p.D) * kWave)) return false;
   *bytes = keys.bytes + rows.bytes;
   return true;
 }
@@ -58,7 +65,7 @@ bool plan_paged_attn_mx4(int dtype, const PagedAttn& p, size_t* bytes) {
 hipError_t launch_paged_attn_mx4(int dtype, const PagedAttn& p, const Mx4Rows& k, const Mx4Rows& v,
                                  void* ws, hipStream_t stream) {
   const Plan keys = keys_of(dtype, p), rows = rows_of(dtype, p, keys);
-  const AttnMx4Args m = {attn_args(p), k, v};
+  const AttnMx4Args m = {attn_args(p), k, v, FastDiv::make(p.hkv), {}};
   return dtype == 1 ? launch<uint16_t>(m, keys, rows, ws, stream)
                     : launch<float>(m, keys, rows, ws, stream);
 }
