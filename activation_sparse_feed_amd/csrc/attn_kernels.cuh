@@ -578,17 +578,42 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys(AttnArgs
 template <typename T, int TM>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   constexpr int kShare = TM == 32 ? 4 : 1;  // waves of a row
+  constexpr int kAhead = 8;                 // loads of a lane in flight
   __shared__ f32x4_t sums[kShare][kWave];
   const PagedAttn& p = a.p;
   const int hk = (int)blockIdx.x % p.hkv, t = (int)blockIdx.x / p.hkv;
+  const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
+  int width = 1;  // lanes of one split's outputs
+  while (width * 4 < p.D) width *= 2;
+  const int side = kWave / width, sub = lane / width, d = (lane & (width - 1)) * 4;
+  const int s_first = kShare == 4 ? wave * side : 0, s_step = side * kShare;
+  // rows from the tile's first: where their parts lie does not depend on the lengths
+  const int seq = TM == 32 ? t / a.tiles_per_seq : 0, tile_row = TM == 32 ? (t - seq * a.tiles_per_seq) * 32 : 0;
+  const size_t slots = TM == 32 ? ((size_t)seq * p.hkv + hk) * a.slot_rows + tile_row
+                                : ((size_t)t * p.hkv + hk) * TM;
+  const int i_first = kShare == 4 ? (int)blockIdx.y : (int)blockIdx.y * 4 + wave;
+  const float* const outputs = a.part_o + (d < p.D ? d : 0);
+  float m_ahead = -INFINITY, l_ahead = 0.f;
+  f32x4_t o_ahead[kAhead];
+  const bool early = a.early != 0 && (TM == 32 ? tile_row + i_first < a.slot_rows : i_first < TM);
+  if (early) {
+    const size_t slot = slots + i_first;
+    const size_t at = (size_t)min(lane, a.splits - 1) * a.part_rows + slot;
+    m_ahead = a.part_ml[2 * at];
+    l_ahead = a.part_ml[2 * at + 1];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (s_first + k * s_step < a.splits)
+        o_ahead[k] = *(const f32x4_t*)(outputs + ((size_t)min(s_first + k * s_step + sub, a.splits - 1) *
+                                                  a.part_rows + slot) * p.D);
+  }
   Work w;
   int n;
   if constexpr (TM == 32) {
     KeysWork k;
-    const int s = t / a.tiles_per_seq;
-    read_sequence(p, s, &k.w);
+    read_sequence(p, seq, &k.w);
     const int all = k.w.nq * a.g;
-    k.w.tile = t - s * a.tiles_per_seq;
+    k.w.tile = t - seq * a.tiles_per_seq;
     if (k.w.tile * 32 >= all || all > a.max_rows) return;
     sequence_range(a, &k);
     n = k.n_split;
@@ -605,19 +630,15 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
     n = split_range(a, 0, lo, hi, &b, &e);
   }
   if (n == 1) return;  // written by the kernel before
-  const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
-  int width = 1;  // lanes of one split's outputs
-  while (width * 4 < p.D) width *= 2;
-  const int side = kWave / width, sub = lane / width, d = (lane & (width - 1)) * 4;
-  const int first = r0 + (kShare == 4 ? (int)blockIdx.y : (int)blockIdx.y * 4 + wave);
-  for (int r = first; r <= r1; r += (int)gridDim.y * (4 / kShare)) {
-    const size_t slot = TM == 32 ? ((size_t)w.seq * p.hkv + hk) * a.slot_rows + r
-                                 : ((size_t)t * p.hkv + hk) * TM + (r - r0);
+  for (int i = i_first; r0 + i <= r1; i += (int)gridDim.y * (4 / kShare)) {
+    const int r = r0 + i;
+    const bool ahead = early && i == i_first;
+    const size_t slot = slots + i;
     float ms = -INFINITY, ls = 0.f;
     if (lane < n) {
       const size_t at = lane * a.part_rows + slot;
-      ms = a.part_ml[2 * at];
-      ls = a.part_ml[2 * at + 1];
+      ms = ahead ? m_ahead : a.part_ml[2 * at];
+      ls = ahead ? l_ahead : a.part_ml[2 * at + 1];
     }
     float m = ms;
 #pragma unroll
@@ -625,18 +646,25 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
     const float f = ms == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms - m);
     const float l = wave_sum(f * ls);
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-    const float* o = a.part_o + slot * p.D + (d < p.D ? d : 0);
-    // loads without conditions, so that they are in flight together: a split past the
-    // last one reads it again and drops it.  A factor of 0 drops nothing: NaN times it
-    // stays NaN, as in a sum over all keys
-#pragma unroll 8
-    for (int s0 = kShare == 4 ? wave * side : 0; s0 < n; s0 += side * kShare) {
-      const int s = s0 + sub, sc = min(s, n - 1);
-      const float fs = __shfl(f, sc, kWave);
-      const f32x4_t x = *(const f32x4_t*)(o + (size_t)sc * a.part_rows * p.D);
+    // a split past the last one is dropped.  A factor of 0 drops nothing: NaN times it stays
+    // NaN, as in a sum over all keys
+    auto add = [&](int s0, const f32x4_t& x) __attribute__((always_inline)) {
+      const int s = s0 + sub;
+      const float fs = __shfl(f, min(s, n - 1), kWave);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] += s < n ? fs * x[i] : 0.f;
+    };
+    int s0 = s_first;
+    if (ahead) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (s_first + k * s_step < n) add(s_first + k * s_step, o_ahead[k]);
+      s0 += kAhead * s_step;
     }
+    // loads without conditions, so that they are in flight together
+#pragma unroll 8
+    for (; s0 < n; s0 += s_step)
+      add(s0, *(const f32x4_t*)(outputs + ((size_t)min(s0 + sub, n - 1) * a.part_rows + slot) * p.D));
     for (int k = width; k < kWave; k <<= 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], k, kWave);

@@ -492,13 +492,13 @@ struct KeysLoader {
 constexpr int keys_mx4_rows(int elt_bytes, int head_dim, int64_t rows) {
   return rows > 16 && elt_bytes == 2 && head_dim <= 128 ? 32 : 16;
 }
-// Waves of a workgroup.
-#ifndef SFFN_NW
-#define SFFN_NW 8
-#endif
-constexpr int keys_mx4_waves(int elt_bytes, int head_dim) {
-  return elt_bytes == 4 && head_dim > 128 ? 4 : SFFN_NW;
-}
+// Waves of a workgroup: eight where the longest key range that its tiles can see is short
+// enough for eight to walk over it in five steps, so that it is not split, four otherwise.
+// 24 drafts in a window of 1000 (8 heads a key head, width 64): 9.8 us, in splits of four
+// waves and a join 18.7; but split ranges of 32 tokens over up to 4096 keys: 22.8 us with four
+// waves, 26.0 with eight; float32 chunks (of 16 rows) 78.0 and 80.8.
+constexpr int kKeysWhole = 8 * 32 * 5;
+constexpr int keys_mx4_waves(int elt_bytes, int64_t span) { return elt_bytes == 2 && span <= kKeysWhole ? 8 : 4; }
 // Waves of a SIMD that the registers are meant for.
 constexpr int keys_mx4_occupancy(int elt_bytes, int dp, int row_tiles, bool compact) {
   if (elt_bytes == 4) return dp > 128 ? 1 : 2;
@@ -691,7 +691,8 @@ __global__ __launch_bounds__(NW * 64, keys_mx4_occupancy(sizeof(T), DP, RT, COMP
 // Launches of one element type, in files of their own.  near: rows can be looked up by 16.
 template <typename T> hipError_t launch_attn_rows_mx4(const AttnMx4Args& m, bool near, hipStream_t s);
 template <typename T>
-hipError_t launch_attn_keys_mx4(const AttnMx4Args& m, int tile_rows, bool near, bool compact, hipStream_t s);
+hipError_t launch_attn_keys_mx4(const AttnMx4Args& m, int tile_rows, int waves, bool near, bool compact,
+                                hipStream_t s);
 
 template <typename T, int DP>
 hipError_t attn_rows_mx4_width(const AttnMx4Args& m, bool near, hipStream_t s) {
@@ -703,9 +704,8 @@ hipError_t attn_rows_mx4_width(const AttnMx4Args& m, bool near, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int DP, int RT, int G, bool WHOLE>
+template <typename T, int DP, int RT, int G, bool WHOLE, int kWaves>
 hipError_t attn_keys_mx4_go(const AttnMx4Args& m, bool compact, hipStream_t s) {
-  constexpr int kWaves = keys_mx4_waves(sizeof(T), DP);
   const AttnArgs& a = m.a;
   const int64_t items = (int64_t)a.n_tiles * a.p.hkv * a.splits, most = 2 * kCus;
   const dim3 all((unsigned)(a.n_tiles * a.p.hkv), (unsigned)a.splits);
@@ -715,19 +715,26 @@ hipError_t attn_keys_mx4_go(const AttnMx4Args& m, bool compact, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int DP, int RT>
+template <typename T, int DP, int RT, int kWaves>
 hipError_t attn_keys_mx4_rows(const AttnMx4Args& m, bool near, bool compact, hipStream_t s) {
-  if (!near) return attn_keys_mx4_go<T, DP, RT, 0, false>(m, compact, s);
-  return m.a.p.D == DP ? attn_keys_mx4_go<T, DP, RT, 16, true>(m, compact, s)
-                       : attn_keys_mx4_go<T, DP, RT, 16, false>(m, compact, s);
+  if (!near) return attn_keys_mx4_go<T, DP, RT, 0, false, kWaves>(m, compact, s);
+  return m.a.p.D == DP ? attn_keys_mx4_go<T, DP, RT, 16, true, kWaves>(m, compact, s)
+                       : attn_keys_mx4_go<T, DP, RT, 16, false, kWaves>(m, compact, s);
 }
 
-// tile_rows: of keys_mx4_rows.
+// tile_rows: of keys_mx4_rows; waves: of keys_mx4_waves.
 template <typename T, int DP>
-hipError_t attn_keys_mx4_width(const AttnMx4Args& m, int tile_rows, bool near, bool compact, hipStream_t s) {
-  if constexpr (keys_mx4_rows(sizeof(T), DP, 32) == 32)
-    if (tile_rows == 32) return attn_keys_mx4_rows<T, DP, 2>(m, near, compact, s);
-  return attn_keys_mx4_rows<T, DP, 1>(m, near, compact, s);
+hipError_t attn_keys_mx4_width(const AttnMx4Args& m, int tile_rows, int waves, bool near, bool compact,
+                               hipStream_t s) {
+  if constexpr (keys_mx4_rows(sizeof(T), DP, 32) == 32) {
+    if (tile_rows == 32)
+      return waves == 8 ? attn_keys_mx4_rows<T, DP, 2, 8>(m, near, compact, s)
+                        : attn_keys_mx4_rows<T, DP, 2, 4>(m, near, compact, s);
+  }
+  if constexpr (sizeof(T) == 2) {
+    if (waves == 8) return attn_keys_mx4_rows<T, DP, 1, 8>(m, near, compact, s);
+  }
+  return attn_keys_mx4_rows<T, DP, 1, 4>(m, near, compact, s);
 }
 
 }  // namespace sffn

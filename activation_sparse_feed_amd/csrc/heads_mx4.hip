@@ -168,7 +168,7 @@ template <typename T, int V> struct KeyRotation {
     if (p.norm) {
       double ss = 0.0;
       if (live) {
-#pragma unroll 1
+#pragma unroll 4
         for (int i = 0; i < kPiece; ++i) {
           const double x = Elt<T>::load1(row, at + i);
           ss += x * x;
@@ -182,7 +182,7 @@ template <typename T, int V> struct KeyRotation {
     const bool known = pos >= 0 && pos < p.max_pos;
     const float* angles = p.table + (size_t)(known ? pos : 0) * p.rot;
     const int half = p.rot / 2;
-#pragma unroll 1
+#pragma unroll 2
     for (int i = 0; i < kPiece; ++i) {
       const int e = at + i;
       double n = (double)Elt<T>::load1(row, e) * r;

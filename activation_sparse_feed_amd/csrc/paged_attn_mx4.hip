@@ -9,16 +9,19 @@ namespace sffn {
 
 template <> hipError_t launch_attn_rows_mx4<uint16_t>(const AttnMx4Args&, bool, hipStream_t);
 template <> hipError_t launch_attn_rows_mx4<float>(const AttnMx4Args&, bool, hipStream_t);
-template <> hipError_t launch_attn_keys_mx4<uint16_t>(const AttnMx4Args&, int, bool, bool, hipStream_t);
-template <> hipError_t launch_attn_keys_mx4<float>(const AttnMx4Args&, int, bool, bool, hipStream_t);
+template <> hipError_t launch_attn_keys_mx4<uint16_t>(const AttnMx4Args&, int, int, bool, bool, hipStream_t);
+template <> hipError_t launch_attn_keys_mx4<float>(const AttnMx4Args&, int, int, bool, bool, hipStream_t);
 
 namespace {
 
 int tile_of(int dtype, const PagedAttn& p) {
   return keys_mx4_rows(dtype == 1 ? 2 : 4, p.D, p.max_q * (int64_t)(p.hq / p.hkv));
 }
+int waves_of(int dtype, const PagedAttn& p) {
+  return keys_mx4_waves(dtype == 1 ? 2 : 4, key_span(p, keys_max(p) / (p.hq / p.hkv) + 1));
+}
 Plan keys_of(int dtype, const PagedAttn& p) {
-  const int step = keys_mx4_waves(dtype == 1 ? 2 : 4, p.D) * 32, tile = tile_of(dtype, p);
+  const int step = waves_of(dtype, p) * 32, tile = tile_of(dtype, p);
   return plan_keys(p, dtype == 1 ? KeysTuning{step * 5, step * 2, step * 6, 4 * kCus, tile}
                                  : KeysTuning{step * 2, step, step, 4 * kCus, tile});
 }
@@ -45,7 +48,7 @@ hipError_t launch(AttnMx4Args m, const Plan& keys, const Plan& rows, void* ws, h
   if (keys.used) {
     place(&a, keys, ws);
     m.tiles = FastDiv::make(a.tiles_per_seq);
-    e = launch_attn_keys_mx4<T>(m, tile_of(dtype, a.p), near, rows.used, s);
+    e = launch_attn_keys_mx4<T>(m, tile_of(dtype, a.p), waves_of(dtype, a.p), near, rows.used, s);
     if (e == hipSuccess) e = launch_join(dtype, kKeysTile, a, keys, s);
   }
   return e;
@@ -57,7 +60,7 @@ bool plan_paged_attn_mx4(int dtype, const PagedAttn& p, size_t* bytes) {
   *bytes = 0;
   if (p.T == 0 || p.n_seqs == 0 || p.max_q == 0) return true;  // nothing is launched
   const Plan keys = keys_of(dtype, p), rows = rows_of(dtype, p, keys);
-  if (!plan_fits(keys, rows, p, keys_mx4_waves(dtype == 1 ? 2 : 4, p.D) * kWave)) return false;
+  if (!plan_fits(keys, rows, p, waves_of(dtype, p) * kWave)) return false;
   *bytes = keys.bytes + rows.bytes;
   return true;
 }
