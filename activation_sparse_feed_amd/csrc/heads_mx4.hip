@@ -275,6 +275,11 @@ __device__ __forceinline__ void store_rows(const HeadsFwd& p, const Mx4Rows& kc,
       // the least and the most that the results can be give the same codes under one scale,
       // or this is done in 64 bits; what is not finite makes the bounds so, too
       float far = rot.apply(p, G, xk[i], yk[i], e), lo[kPiece], hi[kPiece];
+      if (at >= p.D) {  // nothing of a row: 0 times an infinite r is not 0
+        far = 0.f;
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) e[j] = 0.f;
+      }
 #pragma unroll
       for (int j = 0; j < kPiece; ++j) lo[j] = e[j] - far, hi[j] = e[j] + far;
       far = fmaxf(far, dpp_f32<0xB1>(far));

@@ -700,28 +700,45 @@ class PagedAttention:
     shape (T new tokens of n_seqs sequences).  ``forward`` issues paged_kv_append
     and paged_attn_fwd on one stream with no host synchronisation.  The caches
     may be given (``k_cache``, ``v_cache``), e.g. to use them with several batch
-    shapes."""
+    shapes.  With ``mx4`` the cache is a 4-bit one, a new one (True) or the one given
+    (an ``Mx4Cache``, kept as ``cache``), and the entry points are those of that form."""
 
     def __init__(self, T: int, n_seqs: int, n_q_heads: int, n_kv_heads: int, head_dim: int, dtype,
                  page_size: int, n_pages: int, max_pages: int, max_q: int, max_kv: int,
                  rot_dim: int = 0, max_pos: int = 0, norm: bool = False, eps: float = 1e-6,
                  adjacent: bool = False, causal: bool = True, window: int = 0,
-                 scale: float | None = None, k_cache=None, v_cache=None, device="cuda"):
+                 scale: float | None = None, k_cache=None, v_cache=None, device="cuda",
+                 mx4: bool | Mx4Cache = False):
         self.heads = make_heads(T, n_q_heads, n_kv_heads, head_dim, dtype, rot_dim, max_pos, norm,
                                 eps, adjacent)
         self.batch = make_paged_batch(T, n_seqs, n_q_heads, n_kv_heads, head_dim, dtype, page_size,
                                       n_pages, max_pages, max_q, max_kv, causal, window, scale)
         dt = _TORCH_DTYPE[self.heads.dtype]
-        shape = (n_pages, page_size, n_kv_heads, head_dim)
-        self.k_cache = torch.empty(shape, dtype=dt, device=device) if k_cache is None else k_cache
-        self.v_cache = torch.empty(shape, dtype=dt, device=device) if v_cache is None else v_cache
+        self.cache = self.k_cache = self.v_cache = None
+        if mx4:
+            if k_cache is not None or v_cache is not None:
+                raise ValueError("a 4-bit cache is given as mx4, not as k_cache and v_cache")
+            self.cache = mx4 if isinstance(mx4, Mx4Cache) else \
+                Mx4Cache(n_pages, page_size, n_kv_heads, head_dim, device)
+            self.cache._check("PagedAttention", n_pages, page_size, n_kv_heads, head_dim)
+        else:
+            shape = (n_pages, page_size, n_kv_heads, head_dim)
+            self.k_cache = torch.empty(shape, dtype=dt, device=device) if k_cache is None else k_cache
+            self.v_cache = torch.empty(shape, dtype=dt, device=device) if v_cache is None else v_cache
         self.q_out = torch.empty((T, n_q_heads, head_dim), dtype=dt, device=device)
         self.out = torch.empty((T, n_q_heads, head_dim), dtype=dt, device=device)
         self.lse = torch.empty((T, n_q_heads), dtype=torch.float32, device=device)
-        self.workspace = alloc_paged_workspace(self.batch, device)
+        self.workspace = alloc_paged_mx4_workspace(self.batch, device) if mx4 else \
+            alloc_paged_workspace(self.batch, device)
 
     def forward(self, q, k, v, positions, slots, q_start, kv_len, block_table, table=None,
                 q_weight=None, k_weight=None, stream=None) -> torch.Tensor:
+        if self.cache is not None:
+            paged_kv_append_mx4(self.heads, q, k, v, q_weight, k_weight, table, positions, slots,
+                                self.q_out, self.cache, stream)
+            paged_attn_mx4_fwd(self.batch, self.q_out, self.cache, q_start, kv_len, block_table,
+                               self.out, self.workspace, self.lse, stream)
+            return self.out
         paged_kv_append(self.heads, q, k, v, q_weight, k_weight, table, positions, slots,
                         self.q_out, self.k_cache, self.v_cache, stream)
         paged_attn_fwd(self.batch, self.q_out, self.k_cache, self.v_cache, q_start, kv_len,

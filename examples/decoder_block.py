@@ -2,12 +2,14 @@
 activation-sparse FFN.
 
     python examples/decoder_block.py            # serve: prompts in chunks, then tokens
+    python examples/decoder_block.py --mx4      # the same with a 4-bit cache
     python examples/decoder_block.py --train    # train: a few steps of the head norms
 
 Serving runs sequences of different lengths together: each step appends the new
 tokens' keys and values to the cache (heads normalised and rotated on the way),
 attends, projects, and passes through the sparse FFN.  At the end the block is
-computed once more for whole sequences, in plain float32, and compared.
+computed once more for whole sequences, in plain float32, and compared; with a 4-bit
+cache over the keys and values that such a cache holds.
 Training fits the norm weights of q and k to a teacher's, with the library's
 forward and backward behind torch's autograd.  The projections are torch
 products; weights are random.
@@ -56,15 +58,19 @@ class Server:
     """The block's cache and its steps.  A step's shape (tokens, sequences) fixes
     its buffers; they are kept by shape."""
 
-    def __init__(self, block: Block, lengths, page_size=16):
+    def __init__(self, block: Block, lengths, page_size=16, mx4=False):
         self.b, self.page = block, page_size
         self.max_pages = max(-(-n // page_size) for n in lengths)
         n_pages = self.max_pages * len(lengths)
         # every sequence's pages, scattered over the cache
         self.pages = torch.randperm(n_pages, device="cuda").to(torch.int32).view(len(lengths), -1)
-        shape = (n_pages, page_size, block.hkv, block.dim)
-        self.k = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
-        self.v = torch.empty_like(self.k)
+        self.n_pages = n_pages
+        if mx4:
+            self.cache = {"mx4": sffn.Mx4Cache(n_pages, page_size, block.hkv, block.dim)}
+        else:
+            shape = (n_pages, page_size, block.hkv, block.dim)
+            self.cache = {n: torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+                          for n in ("k_cache", "v_cache")}
         self.done = [0] * len(lengths)
         self.shapes = {}
 
@@ -74,9 +80,9 @@ class Server:
         key = (T, len(seqs), max(counts))
         if key not in self.shapes:
             attn = sffn.PagedAttention(
-                T, len(seqs), b.hq, b.hkv, b.dim, torch.bfloat16, self.page, self.k.shape[0],
+                T, len(seqs), b.hq, b.hkv, b.dim, torch.bfloat16, self.page, self.n_pages,
                 self.max_pages, max(counts), self.max_pages * self.page, rot_dim=b.dim,
-                max_pos=b.max_pos, norm=True, eps=EPS, k_cache=self.k, v_cache=self.v)
+                max_pos=b.max_pos, norm=True, eps=EPS, **self.cache)
             self.shapes[key] = attn, sffn.SparseFFN(T, b.d_model, b.d_ff, 32, torch.bfloat16)
         attn, ffn = self.shapes[key]
         pos, seq, starts = [], [], [0]
@@ -96,10 +102,24 @@ class Server:
         return x + ffn.forward(rms(x), b.wg, b.bg, b.wu, b.wd)
 
 
-def plain(b: Block, x):
+def held(b: Block, qkv):
+    """The keys (normalised and rotated) and values of one sequence that a 4-bit cache holds."""
+    T = qkv.shape[0]
+    cache = sffn.Mx4Cache(1, T, b.hkv, b.dim)
+    heads = sffn.make_heads(T, 0, b.hkv, b.dim, torch.bfloat16, b.dim, b.max_pos, True, EPS)
+    rows = torch.arange(T, dtype=torch.int32, device="cuda")
+    sffn.paged_kv_append_mx4(heads, None, qkv[:, b.hq:b.hq + b.hkv], qkv[:, b.hq + b.hkv:], None,
+                             b.k_norm, b.table, rows, rows, None, cache)
+    k, v = (torch.empty((T, b.hkv, b.dim), device="cuda") for _ in range(2))
+    sffn.paged_kv_read_mx4(cache, rows, k, v)
+    return k, v
+
+
+def plain(b: Block, x, mx4=False):
     """The block over one whole sequence, float32."""
     T = x.shape[0]
-    qkv = (rms(x) @ b.qkv).float().view(T, -1, b.dim)
+    raw = (rms(x) @ b.qkv).view(T, -1, b.dim)
+    qkv = raw.float()
 
     def rotated(h, w):
         h = h * torch.rsqrt(h.square().mean(-1, keepdim=True) + EPS) * w.float()
@@ -109,8 +129,9 @@ def plain(b: Block, x):
 
     g = b.hq // b.hkv
     q = rotated(qkv[:, :b.hq], b.q_norm).permute(1, 0, 2)
-    k = rotated(qkv[:, b.hq:b.hq + b.hkv], b.k_norm).permute(1, 2, 0).repeat_interleave(g, 0)
-    v = qkv[:, b.hq + b.hkv:].permute(1, 0, 2).repeat_interleave(g, 0)
+    k, v = held(b, raw) if mx4 else (rotated(qkv[:, b.hq:b.hq + b.hkv], b.k_norm), qkv[:, b.hq + b.hkv:])
+    k = k.permute(1, 2, 0).repeat_interleave(g, 0)
+    v = v.permute(1, 0, 2).repeat_interleave(g, 0)
     p = q.contiguous() @ k.contiguous() * b.dim ** -0.5
     p = p.masked_fill(torch.ones(T, T, dtype=torch.bool, device="cuda").triu(1), -torch.inf).softmax(-1)
     x = x + ((p @ v.contiguous()).permute(1, 0, 2).reshape(T, -1) @ b.proj.float()).to(x.dtype)
@@ -119,7 +140,7 @@ def plain(b: Block, x):
     return x + (h @ b.wd.float()).to(x.dtype)
 
 
-def serve(lengths=(150, 37, 90), chunk=48, tokens=6, seed=0):
+def serve(lengths=(150, 37, 90), chunk=48, tokens=6, seed=0, mx4=False):
     """Prompts of `lengths` in chunks, a sequence that is through its prompt taking
     single tokens meanwhile; returns the largest relative error of a sequence."""
     b = Block(seed=seed)
@@ -127,7 +148,7 @@ def serve(lengths=(150, 37, 90), chunk=48, tokens=6, seed=0):
     g = torch.Generator(device="cuda")
     g.manual_seed(seed + 1)
     xs = [torch.randn((n, b.d_model), generator=g, device="cuda").to(torch.bfloat16) for n in total]
-    srv = Server(b, total)
+    srv = Server(b, total, mx4=mx4)
     ys = [[] for _ in total]
     while any(d < n for d, n in zip(srv.done, total)):
         seqs = [s for s, n in enumerate(total) if srv.done[s] < n]
@@ -138,7 +159,7 @@ def serve(lengths=(150, 37, 90), chunk=48, tokens=6, seed=0):
             ys[s].append(part)
     worst = 0.0
     for x, y in zip(xs, ys):
-        want, got = plain(b, x).float() - x.float(), torch.cat(y).float() - x.float()
+        want, got = plain(b, x, mx4).float() - x.float(), torch.cat(y).float() - x.float()
         worst = max(worst, ((got - want).norm() / want.norm()).item())
     return worst
 
@@ -196,11 +217,13 @@ def train(steps=60, T=256, lr=0.1, seed=0):
 def main():
     p = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     p.add_argument("--train", action="store_true")
-    if p.parse_args().train:
+    p.add_argument("--mx4", action="store_true", help="serve with a 4-bit cache")
+    args = p.parse_args()
+    if args.train:
         first, last = train()
         print(f"loss of the head norms: {first:.3e} -> {last:.3e}")
     else:
-        print(f"served against whole sequences: relative error {serve():.2e}")
+        print(f"served against whole sequences: relative error {serve(mx4=args.mx4):.2e}")
 
 
 if __name__ == "__main__":
