@@ -26,46 +26,72 @@ struct AttnMx4Args {
   AttnArgs a;
   Mx4Rows k, v;
   FastDiv heads, tiles;  // key heads; attn_keys_mx4: tiles_per_seq
+  int alike;             // see RowPlace
 };
 
-// Words of codes at p (4-byte aligned); `at`: the element that the first belongs to.
-// Elements from D on read as 0.
+// Words of codes of a row's elements at, at + 8, ...; row: its first word (4-byte aligned).  In
+// place of elements from head_dim on the row's last ones are read: queries are 0 there, and
+// such elements of the output are dropped.
 template <int W, bool WHOLE>
-__device__ __forceinline__ void load_codes(const uint8_t* p, int at, int D, uint32_t (&w)[W]) {
+__device__ __forceinline__ void load_codes(const uint8_t* row, int at, int D, uint32_t (&w)[W]) {
   if constexpr (WHOLE) {
     constexpr int kN = W < 4 ? W : 4;
     typedef uint32_t vec_t __attribute__((ext_vector_type(kN), aligned(4)));
 #pragma unroll
     for (int i = 0; i < W; i += kN) {
-      if constexpr (kN == 1) {
-        w[i] = *(const uint32_t*)(p + 4 * i);
-      } else {
-        const vec_t v = *(const vec_t*)(p + 4 * i);
+      const vec_t v = *(const vec_t*)(row + at / 2 + 4 * i);
 #pragma unroll
-        for (int j = 0; j < kN; ++j) w[i + j] = v[j];
-      }
+      for (int j = 0; j < kN; ++j) w[i + j] = v[j];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = at + 8 * i < D ? *(const uint32_t*)(p + 4 * i) : 0u;
+    for (int i = 0; i < W; ++i) w[i] = *(const uint32_t*)(row + min(at + 8 * i, D - 8) / 2);
   }
 }
 
-// The scale bytes at p, of the blocks from number b on; 127 (a scale of 1) beyond the head.
+// The scale bytes of a row's blocks from number b on, with the last one's beyond it.
 template <int B, bool WHOLE>
-__device__ __forceinline__ void load_scales(const uint8_t* p, int b, int n_blocks, uint32_t (&s)[B]) {
+__device__ __forceinline__ void load_scales(const uint8_t* row, int b, int n_blocks, uint32_t (&s)[B]) {
 #pragma unroll
-  for (int i = 0; i < B; ++i) s[i] = WHOLE || b + i < n_blocks ? p[i] : 127u;
+  for (int i = 0; i < B; ++i) s[i] = row[WHOLE ? b + i : min(b + i, n_blocks - 1)];
+}
+
+// float32 queries: a value and its rest in bfloat16, three of them exactly the 24 bits that
+// float32 has (cut off, not rounded, so that nothing overflows).  What a 4-bit cache holds
+// is bfloat16, so a product with float32 is three with bfloat16 and their sum, all in
+// float32: five times as fast as on the float32 matrix instructions, and as exact.
+__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+// The upper halves of two: the second in the upper half of the result.
+__device__ __forceinline__ uint32_t pack_cut(float a, float b) {
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+// Parts 0 .. 2 of pairs of values, largest first.  An infinite or NaN one has no rest.
+template <int N>
+__device__ __forceinline__ void split_parts(const float (&x)[2 * N], uint32_t (&o)[3][N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float r[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float v = x[2 * i + j];  // a NaN is a quiet one: it stays one when it is cut
+      const bool fine = (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u;
+      r[0][j] = fine ? v - cut(v) : 0.f;
+      r[1][j] = r[0][j] - cut(r[0][j]);
+    }
+    o[0][i] = pack_cut(x[2 * i], x[2 * i + 1]);
+    o[1][i] = pack_cut(r[0][0], r[0][1]);
+    o[2][i] = pack_cut(r[1][0], r[1][1]);
+  }
 }
 
 // ------------------------------------------------------------------ many rows
 // Where a row of codes and its scales lie.
-//   G = 16  page_size is a multiple of 16, and K and V have the same strides, of less than
-//           2^24 bytes for a token and 2^31 for a page: a wave's 16 (or 8) neighbouring rows lie
-//           in one page, which is looked up with scalar instructions, and a lane adds an
-//           offset that never changes.
-//   G = 0   any page size and strides: a lane looks up its own row.  Its 64-bit products
-//           cost more than everything else that a wave does for its keys.
+//   G = 16  page_size is a multiple of 16 and the caches are alike: a wave's 16 (or 8)
+//           neighbouring rows lie in one page, which is looked up with scalar instructions,
+//           and a lane adds an offset that never changes.
+//   G = 0   any page size and strides: a lane looks up its own row.
+// Caches are alike where K and V have the same strides, of less than 2^24 bytes for a token
+// and 2^31 for a page.
 template <int G>
 struct RowPlace {
   int page, off;
@@ -79,20 +105,25 @@ struct RowPlace {
     if constexpr (G > 0) page = load_uniform(bt + pg);
     else page = bt[pg];
   }
-  // Bytes from the start of the cache to that row.
-  __device__ __forceinline__ int64_t bytes(int last_page, int64_t page_bytes, int64_t token_bytes) const {
+  // Bytes from the start of the cache to that row, near: strides of alike caches.
+  __device__ __forceinline__ uint64_t near(int last_page, int64_t page_bytes, int64_t token_bytes) const {
     const uint32_t pg = (uint32_t)min(max(page, 0), last_page);
-    if constexpr (G > 0)
-      return (int64_t)((uint64_t)pg * (uint32_t)page_bytes + (uint64_t)(uint32_t)off * (uint32_t)token_bytes);
-    else return (int64_t)pg * page_bytes + off * token_bytes;
+    return (uint64_t)pg * (uint32_t)page_bytes + (uint64_t)(uint32_t)off * (uint32_t)token_bytes;
+  }
+  __device__ __forceinline__ uint64_t far(int last_page, int64_t page_bytes, int64_t token_bytes) const {
+    return min(max(page, 0), last_page) * page_bytes + off * token_bytes;
+  }
+  __device__ __forceinline__ uint64_t bytes(int last_page, int64_t page_bytes, int64_t token_bytes) const {
+    return G > 0 ? near(last_page, page_bytes, token_bytes) : far(last_page, page_bytes, token_bytes);
   }
 };
 
 // Tiles of KT rows of one cache: every thread has kPer elements of one row of a tile.  Pages
 // are looked up two tiles ahead, codes loaded one ahead, and turned into values in LDS
-// in the layout of AttnTile (elements from head_dim to the end of an LDS row: 0).
-template <typename T, int DP, int KT, int NT, int G, bool K>
+// in the layout of AttnTile (from head_dim to the end of an LDS row: the row's last elements).
+template <int DP, int KT, int NT, int G, bool WHOLE, bool K>
 struct Mx4Loader {
+  typedef uint16_t T;  // of the values in LDS
   typedef AttnTile<T, DP, KT> Tile;
   static constexpr int kPer = KT * Tile::kRowElems / NT;
   static constexpr int kParts = Tile::kRowElems / kPer;  // threads of a row
@@ -115,8 +146,8 @@ struct Mx4Loader {
     scales = c.scales + hk * c.s_head;
     page_bytes = c.page, token_bytes = c.token, s_page = c.s_page, s_token = c.s_token;
     const int r = G > 0 ? lane_id() / kParts : 0;
-    lane_codes = (uint32_t)r * (uint32_t)c.token + part * (kPer / 2);
-    lane_scales = (uint32_t)r * (uint32_t)c.s_token + part * kPer / kMxBlock;
+    lane_codes = (uint32_t)r * (uint32_t)c.token + (WHOLE ? part * (kPer / 2) : 0);
+    lane_scales = (uint32_t)r * (uint32_t)c.s_token + (WHOLE ? part * kPer / kMxBlock : 0);
     per_page = a.page;
     last_page = a.p.n_pages - 1;
     first = lo, last = hi - 1;
@@ -135,13 +166,8 @@ struct Mx4Loader {
   __device__ __forceinline__ void start() {
     const uint8_t* c = codes + at.bytes(last_page, page_bytes, token_bytes) + lane_codes;
     const uint8_t* b = scales + at.bytes(last_page, s_page, s_token) + lane_scales;
-    if (D == Tile::kRowElems) {
-      load_codes<kW, true>(c, 0, D, w);
-      load_scales<kB, true>(b, 0, 0, s);
-    } else {
-      load_codes<kW, false>(c, part * kPer, D, w);
-      load_scales<kB, false>(b, part * kPer / kMxBlock, mx_blocks(D), s);
-    }
+    load_codes<kW, WHOLE>(c, WHOLE ? 0 : part * kPer, D, w);
+    load_scales<kB, WHOLE>(b, WHOLE ? 0 : part * kPer / kMxBlock, mx_blocks(D), s);
   }
   __device__ __forceinline__ void finish(uint8_t* tile) const {
     const int swz = K ? Tile::swz_k(row) : Tile::swz_v(row);
@@ -158,10 +184,82 @@ struct Mx4Loader {
   }
 };
 
-template <typename T, int DP, int KT, int NW, int G>
-__global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 && NW == 4 ? 2 : 1) void attn_rows_mx4(
+// The tile of the rows kernel: that of a bfloat16 cache, with float32 queries and weights in
+// three parts.
+template <typename T, int DP, int KT> struct RowsTile : AttnTile<uint16_t, DP, KT> {};
+template <int DP, int KT> struct RowsTile<float, DP, KT> : AttnTile<uint16_t, DP, KT> {
+  typedef AttnTile<uint16_t, DP, KT> Base;
+  typedef Frag<uint16_t> F;
+  u32x4_t qs[3][Base::kQ];
+
+  __device__ __forceinline__ void load_q(const float* row, int D) {
+    const int h = lane_id() >> 5;
+#pragma unroll
+    for (int i = 0; i < Base::kQ; ++i) {
+      const int e = (2 * i + h) * 8;
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (e < D) {
+        Elt<float>::unpack(ldg16(row + e), x);
+        Elt<float>::unpack(ldg16(row + e + 4), x + 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __builtin_canonicalizef(x[j]);
+      }
+      uint32_t p[3][4];
+      split_parts<4>(x, p);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) qs[k][i] = u32x4_t{p[k][0], p[k][1], p[k][2], p[k][3]};
+    }
+  }
+  __device__ __forceinline__ void negate() {
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+      for (int i = 0; i < Base::kQ; ++i) qs[k][i] = F::negate(qs[k][i]);
+  }
+  __device__ __forceinline__ f32x16_t scores(const uint8_t* k) const {
+    const int lane = lane_id(), r = lane & 31, h = lane >> 5;
+    const int at = r * Base::kPitch + ((h ^ Base::swz_k(r)) << 4);
+    f32x16_t s;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < Base::kQ; ++i) {
+      const u32x4_t a = *(const u32x4_t*)(k + (at ^ (i << 5)));
+#pragma unroll
+      for (int p = 2; p >= 0; --p) s = F::mma(a, qs[p][i], s);
+    }
+    return s;
+  }
+  __device__ __forceinline__ void accumulate(const uint8_t* v, const f32x16_t& s) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = s[8 * ks + j];
+      uint32_t p[3][4];
+      split_parts<4>(x, p);
+#pragma unroll
+      for (int d = 0; d < Base::kDt; ++d) {
+        const u32x4_t f = Base::v_frag(v, ks, d);
+#pragma unroll
+        for (int k = 2; k >= 0; --k)
+          this->o[d] = F::mma(f, u32x4_t{p[k][0], p[k][1], p[k][2], p[k][3]}, this->o[d]);
+      }
+    }
+  }
+  __device__ __forceinline__ void step(f32x16_t& s, const uint8_t* k_next, const uint8_t* v, float c) {
+    this->raise(s, c);
+    const f32x16_t next = scores(k_next);
+    this->weights(s, c);
+    accumulate(v, s);
+    s = next;
+  }
+};
+
+template <typename T, int DP, int KT, int NW, int G, bool WHOLE>
+__global__ __launch_bounds__(NW * 64, DP <= (sizeof(T) == 2 ? 128 : 64) ? 2 : 1) void attn_rows_mx4(
     AttnMx4Args m) {
-  typedef AttnTile<T, DP, KT> Tile;
+  typedef RowsTile<T, DP, KT> Tile;
   constexpr int TM = NW * 32;
   __shared__ __align__(1024) uint8_t k0[Tile::kTileBytes], k1[Tile::kTileBytes], v0[Tile::kTileBytes],
       v1[Tile::kTileBytes];
@@ -178,8 +276,8 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 && NW == 4 ? 2
   const int b = pl.b, e = pl.e, x = pl.x, y = pl.y;
   Tile tile;
   tile.init();
-  Mx4Loader<T, DP, KT, NW * 64, G, true> load_k;
-  Mx4Loader<T, DP, KT, NW * 64, G, false> load_v;
+  Mx4Loader<DP, KT, NW * 64, G, WHOLE, true> load_k;
+  Mx4Loader<DP, KT, NW * 64, G, WHOLE, false> load_v;
   load_k.init(a, m.k, pl.w.seq, hk, b, e);
   load_v.init(a, m.v, pl.w.seq, hk, b, e);
   // as in attn_rows the K tile beside a V tile is 32 keys ahead of it
@@ -249,21 +347,10 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 && NW == 4 ? 2
 
 // ------------------------------------------------------------------ few rows
 
-template <typename T> struct Frag16;
-template <> struct Frag16<uint16_t> {
-  __device__ static __forceinline__ f32x4_t mma(u32x4_t a, u32x4_t b, f32x4_t c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
-  }
-};
-template <> struct Frag16<float> {
-  __device__ static __forceinline__ f32x4_t mma(u32x4_t a, u32x4_t b, f32x4_t c) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[e]), __uint_as_float(b[e]), c, 0, 0, 0);
-    return c;
-  }
-};
+__device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                 __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
 
 // Over the four lanes with one l % 16.
 __device__ __forceinline__ float max_quads(float v) {
@@ -281,23 +368,19 @@ struct KeysTile {
   static constexpr int kLane = DP / 4;                       // elements of a lane
   static constexpr int kW = kLane / 8;                       // its words of codes
   static constexpr int kB = kLane < kMxBlock ? 1 : kLane / kMxBlock;  // its scales
-  static constexpr int kC = Mx<T>::kChunks;                  // chunks of a word's values
-  static constexpr int kEpc = 16 / (int)sizeof(T);
+  static constexpr int kParts = sizeof(T) == 2 ? 1 : 3;      // of queries and weights
   static constexpr int kDt = DP / 16;                        // 16-wide blocks of the output
-  static constexpr int kPitch = DP * (int)sizeof(T);         // of a row of V in LDS
+  static constexpr int kPitch = DP * 2;                      // of a row of V in LDS
   static constexpr int kVBytes = 32 * kPitch;
   static constexpr int kOutBytes = RT * 16 * DP * 4;
   static constexpr int kLdsBytes = kVBytes > kOutBytes ? kVBytes : kOutBytes;
 
   // Chunk c of row r lies at c ^ swz(r).  Rows are written by 16 lanes, a row each, at one
-  // chunk: eight neighbouring rows get different chunks.  bfloat16 is read as 32 bytes of
-  // four neighbouring rows, float32 as 64 bytes of every fourth row.
-  __device__ static __forceinline__ int swz(int r) {
-    if constexpr (sizeof(T) == 2) return ((r & 3) << 1) | ((r >> 2) & 1);
-    else return (((r >> 2) & 3) << 2) | (r & 3);
-  }
+  // chunk: eight neighbouring rows get different chunks.  They are read as 32 bytes of four
+  // neighbouring rows.
+  __device__ static __forceinline__ int swz(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
 
-  u32x4_t q[RT][kW * kC];
+  u32x4_t q[RT][kParts][kW];
   f32x4_t o[RT][kDt];
   float m[RT], l[RT];
 
@@ -312,23 +395,38 @@ struct KeysTile {
   }
   // Loads without conditions, so that they are in flight together; finish_q once they are
   // all under way.
+  static constexpr int kRaw = kW * (int)sizeof(T) / 2;  // 16-byte loads of a row
   template <bool WHOLE>
-  __device__ __forceinline__ void load_q(int t, const T* row, int D) {
+  __device__ static __forceinline__ void load_q(const T* row, int D, u32x4_t (&raw)[kRaw]) {
+    constexpr int kEpc = 16 / (int)sizeof(T);
     const int e0 = (lane_id() >> 4) * kLane;
 #pragma unroll
-    for (int i = 0; i < kW * kC; ++i) {
-      const int e = e0 + i * kEpc;
-      q[t][i] = ldg16(row + (WHOLE ? e : min(e, D - kEpc)));
-    }
+    for (int i = 0; i < kRaw; ++i) raw[i] = ldg16(row + (WHOLE ? e0 + i * kEpc : min(e0 + i * kEpc, D - kEpc)));
   }
   template <bool WHOLE>
-  __device__ __forceinline__ void finish_q(int t, int D, bool negate) {
+  __device__ __forceinline__ void finish_q(int t, int D, bool negate, const u32x4_t (&raw)[kRaw]) {
     const int e0 = (lane_id() >> 4) * kLane;
-    const uint32_t sign = negate ? (sizeof(T) == 2 ? 0x80008000u : 0x80000000u) : 0u;
+    const uint32_t sign = negate ? 0x80008000u : 0u;
 #pragma unroll
-    for (int i = 0; i < kW * kC; ++i) {
-      if (!WHOLE && e0 + i * kEpc >= D) q[t][i] = u32x4_t{0u, 0u, 0u, 0u};
-      q[t][i] ^= sign;
+    for (int i = 0; i < kW; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        q[t][0][i] = raw[i];
+      } else {
+        float x[8];
+        Elt<float>::unpack(raw[2 * i], x);
+        Elt<float>::unpack(raw[2 * i + 1], x + 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __builtin_canonicalizef(x[j]);
+        uint32_t p[3][4];
+        split_parts<4>(x, p);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) q[t][k][i] = u32x4_t{p[k][0], p[k][1], p[k][2], p[k][3]};
+      }
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        if (!WHOLE && e0 + 8 * i >= D) q[t][k][i] = u32x4_t{0u, 0u, 0u, 0u};
+        q[t][k][i] ^= sign;
+      }
     }
   }
 
@@ -352,25 +450,23 @@ struct KeysTile {
     for (int t = 0; t < RT; ++t) s[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < kW; ++i) {
-      u32x4_t x[kC];
-      Mx<T>::decode8(k.w[i], scale_k(k, i), x);
+      u32x4_t x[1];
+      Mx<uint16_t>::decode8(k.w[i], scale_k(k, i), x);
 #pragma unroll
-      for (int j = 0; j < kC; ++j)
+      for (int p = kParts - 1; p >= 0; --p)
 #pragma unroll
-        for (int t = 0; t < RT; ++t) s[t] = Frag16<T>::mma(x[j], q[t][i * kC + j], s[t]);
+        for (int t = 0; t < RT; ++t) s[t] = mma16(x[0], q[t][p][i], s[t]);
     }
   }
 
   // V rows b * 16 + lane % 16 to LDS.
   __device__ static __forceinline__ void write_v(uint8_t* lds, int b, const Codes& v) {
-    const int lane = lane_id(), r = b * 16 + (lane & 15), c0 = (lane >> 4) * (kW * kC);
+    const int lane = lane_id(), r = b * 16 + (lane & 15), c0 = (lane >> 4) * kW;
 #pragma unroll
     for (int i = 0; i < kW; ++i) {
-      u32x4_t x[kC];
-      Mx<T>::decode8(v.w[i], scale_v(v, i), x);
-#pragma unroll
-      for (int j = 0; j < kC; ++j)
-        *(u32x4_t*)(lds + r * kPitch + (((c0 + i * kC + j) ^ swz(r)) << 4)) = x[j];
+      u32x4_t x[1];
+      Mx<uint16_t>::decode8(v.w[i], scale_v(v, i), x);
+      *(u32x4_t*)(lds + r * kPitch + (((c0 + i) ^ swz(r)) << 4)) = x[0];
     }
   }
 
@@ -378,39 +474,34 @@ struct KeysTile {
   // + i and 16 more: the order in which the B operand takes them when V^T is read alike.
   __device__ __forceinline__ void accumulate(const uint8_t* lds, const f32x4_t (&s)[2][RT]) {
     const int lane = lane_id(), i = lane & 15, g = lane >> 4;
-    if constexpr (sizeof(T) == 2) {
-      u32x4_t pf[RT];
+    u32x4_t pf[RT][kParts];
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
-        pf[t] = u32x4_t{pack_bf16(s[0][t][0], s[0][t][1]), pack_bf16(s[0][t][2], s[0][t][3]),
-                        pack_bf16(s[1][t][0], s[1][t][1]), pack_bf16(s[1][t][2], s[1][t][3])};
-      const int r = 4 * g + (i >> 2);  // swz(r + 16) is swz(r)
-      const int at = r * kPitch + ((((i & 3) >> 1) ^ swz(r)) << 4) + (i & 1) * 8;
-      typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+    for (int t = 0; t < RT; ++t) {
+      if constexpr (sizeof(T) == 2) {
+        pf[t][0] = u32x4_t{pack_bf16(s[0][t][0], s[0][t][1]), pack_bf16(s[0][t][2], s[0][t][3]),
+                           pack_bf16(s[1][t][0], s[1][t][1]), pack_bf16(s[1][t][2], s[1][t][3])};
+      } else {
+        const float x[8] = {s[0][t][0], s[0][t][1], s[0][t][2], s[0][t][3],
+                            s[1][t][0], s[1][t][1], s[1][t][2], s[1][t][3]};
+        uint32_t p[3][4];
+        split_parts<4>(x, p);
 #pragma unroll
-      for (int d = 0; d < kDt; ++d) {
-        const uint8_t* v = lds + (at ^ (d << 5));
-        const s16x4_t x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)v);
-        const s16x4_t x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(v + 16 * kPitch));
-        const u32x4_t f = __builtin_bit_cast(u32x4_t, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-        for (int t = 0; t < RT; ++t) o[t][d] = Frag16<T>::mma(f, pf[t], o[t][d]);
+        for (int k = 0; k < 3; ++k) pf[t][k] = u32x4_t{p[k][0], p[k][1], p[k][2], p[k][3]};
       }
-    } else {
+    }
+    const int r = 4 * g + (i >> 2);  // swz(r + 16) is swz(r)
+    const int at = r * kPitch + ((((i & 3) >> 1) ^ swz(r)) << 4) + (i & 1) * 8;
+    typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+    for (int d = 0; d < kDt; ++d) {
+      const uint8_t* v = lds + (at ^ (d << 5));
+      const s16x4_t x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)v);
+      const s16x4_t x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(v + 16 * kPitch));
+      const u32x4_t f = __builtin_bit_cast(u32x4_t, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = 16 * b + 4 * g + k;
-          const int at = r * kPitch + (((i >> 2) ^ swz(r)) << 4) + (i & 3) * 4;
+      for (int p = kParts - 1; p >= 0; --p)
 #pragma unroll
-          for (int d = 0; d < kDt; ++d) {
-            const float v = *(const float*)(lds + (at ^ (d << 6)));
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-              o[t][d] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, s[b][t][k], o[t][d], 0, 0, 0);
-          }
-        }
+        for (int t = 0; t < RT; ++t) o[t][d] = mma16(f, pf[t][p], o[t][d]);
     }
   }
 
@@ -447,9 +538,10 @@ struct KeysLoader {
   typedef KeysTile<T, DP, RT> Tile;
   const int32_t* bt;
   Mx4Rows k, v;                  // of the key head
-  uint32_t k_lane, v_lane, ks_lane, vs_lane;  // this lane's bytes from the row that was looked up
+  uint32_t lane_codes, lane_scales;  // G > 0: this lane's row, from the one that was looked up
   FastDiv per_page;
   int last_page, first, last, D, e0;
+  bool alike;
   RowPlace<G> at[2];
 
   __device__ __forceinline__ void init(const AttnMx4Args& m, int seq, int hk, int lo, int hi) {
@@ -459,8 +551,8 @@ struct KeysLoader {
     k.codes += hk * k.head, k.scales += hk * k.s_head;
     v.codes += hk * v.head, v.scales += hk * v.s_head;
     const uint32_t r = G > 0 ? lane_id() & 15 : 0;
-    k_lane = r * (uint32_t)k.token + e0 / 2, ks_lane = r * (uint32_t)k.s_token + e0 / kMxBlock;
-    v_lane = r * (uint32_t)v.token + e0 / 2, vs_lane = r * (uint32_t)v.s_token + e0 / kMxBlock;
+    lane_codes = r * (uint32_t)k.token, lane_scales = r * (uint32_t)k.s_token;
+    alike = m.alike != 0;
     per_page = m.a.page;
     last_page = m.a.p.n_pages - 1;
     first = lo, last = hi - 1;
@@ -471,18 +563,22 @@ struct KeysLoader {
     for (int b = 0; b < 2; ++b)
       at[b].look_up(bt, per_page, j0 + 16 * b + (G > 0 ? 0 : lane_id() & 15), first, last);
   }
-  __device__ __forceinline__ void one(const uint8_t* codes, const uint8_t* scales,
-                                      typename Tile::Codes& x) const {
+  __device__ __forceinline__ void one(const uint8_t* codes, const uint8_t* scales, typename Tile::Codes& x) const {
     load_codes<Tile::kW, WHOLE>(codes, e0, D, x.w);
     load_scales<Tile::kB, WHOLE>(scales, e0 / kMxBlock, mx_blocks(D), x.s);
   }
   __device__ __forceinline__ void start(typename Tile::Codes (&kc)[2], typename Tile::Codes (&vc)[2]) const {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      one(k.codes + at[b].bytes(last_page, k.page, k.token) + k_lane,
-          k.scales + at[b].bytes(last_page, k.s_page, k.s_token) + ks_lane, kc[b]);
-      one(v.codes + at[b].bytes(last_page, v.page, v.token) + v_lane,
-          v.scales + at[b].bytes(last_page, v.s_page, v.s_token) + vs_lane, vc[b]);
+      if (G > 0 || alike) {  // one place in both caches, products of 32-bit strides
+        const uint64_t c = at[b].near(last_page, k.page, k.token) + lane_codes;
+        const uint64_t s = at[b].near(last_page, k.s_page, k.s_token) + lane_scales;
+        one(k.codes + c, k.scales + s, kc[b]);
+        one(v.codes + c, v.scales + s, vc[b]);
+      } else {
+        one(k.codes + at[b].far(last_page, k.page, k.token), k.scales + at[b].far(last_page, k.s_page, k.s_token), kc[b]);
+        one(v.codes + at[b].far(last_page, v.page, v.token), v.scales + at[b].far(last_page, v.s_page, v.s_token), vc[b]);
+      }
     }
   }
 };
@@ -587,15 +683,17 @@ __global__ __launch_bounds__(NW * 64, keys_mx4_occupancy(sizeof(T), DP, RT, COMP
       load.start(kc, vc);
       load.look_up(j0 + step);
     }
+    u32x4_t raw[RT][Tile::kRaw];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const int r = r0 + min(16 * t + (lane & 15), rows - 1);
       const int token = a.group.div(r), head = hk * a.g + r - token * a.g;
       key_range(p, w, token, &row_lo[t], &row_hi[t]);
-      tile.template load_q<WHOLE>(t, (const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D);
+      Tile::template load_q<WHOLE>((const T*)p.q + (int64_t)(w.q0 + token) * p.q_token + head * p.q_head, p.D,
+                                   raw[t]);
     }
 #pragma unroll
-    for (int t = 0; t < RT; ++t) tile.template finish_q<WHOLE>(t, p.D, a.negate);
+    for (int t = 0; t < RT; ++t) tile.template finish_q<WHOLE>(t, p.D, a.negate, raw[t]);
     // Blocks of 32 keys.  Once a block's codes have become operands those of the next are
     // loaded in their place: with four waves a SIMD that is enough under way (with a second
     // set of registers and three waves: decode of 32 tokens 25.0 us instead of 23.1, of three
@@ -694,14 +792,21 @@ template <typename T>
 hipError_t launch_attn_keys_mx4(const AttnMx4Args& m, int tile_rows, int waves, bool near, bool compact,
                                 hipStream_t s);
 
-template <typename T, int DP>
-hipError_t attn_rows_mx4_width(const AttnMx4Args& m, bool near, hipStream_t s) {
-  constexpr int kKeys = RowsShape<T, DP>::kKeys, kWaves = RowsShape<T, DP>::kWaves;
+template <typename T, int DP, bool WHOLE>
+hipError_t attn_rows_mx4_go(const AttnMx4Args& m, bool near, hipStream_t s) {
+  constexpr int kKeys = RowsShape<uint16_t, DP>::kKeys, kWaves = RowsShape<uint16_t, DP>::kWaves;
   const AttnArgs& a = m.a;
   const dim3 grid((unsigned)(a.n_tiles * a.p.hkv), (unsigned)a.splits), block(kWaves * 64);
-  if (near) hipLaunchKernelGGL((attn_rows_mx4<T, DP, kKeys, kWaves, 16>), grid, block, 0, s, m);
-  else hipLaunchKernelGGL((attn_rows_mx4<T, DP, kKeys, kWaves, 0>), grid, block, 0, s, m);
+  if (near) hipLaunchKernelGGL((attn_rows_mx4<T, DP, kKeys, kWaves, 16, WHOLE>), grid, block, 0, s, m);
+  else hipLaunchKernelGGL((attn_rows_mx4<T, DP, kKeys, kWaves, 0, WHOLE>), grid, block, 0, s, m);
   return hipGetLastError();
+}
+
+template <typename T, int DP>
+hipError_t attn_rows_mx4_width(const AttnMx4Args& m, bool near, hipStream_t s) {
+  if constexpr (DP == AttnTile<uint16_t, DP, 64>::kRowElems)
+    if (m.a.p.D == DP) return attn_rows_mx4_go<T, DP, true>(m, near, s);
+  return attn_rows_mx4_go<T, DP, false>(m, near, s);
 }
 
 template <typename T, int DP, int RT, int G, bool WHOLE, int kWaves>
@@ -717,7 +822,9 @@ hipError_t attn_keys_mx4_go(const AttnMx4Args& m, bool compact, hipStream_t s) {
 
 template <typename T, int DP, int RT, int kWaves>
 hipError_t attn_keys_mx4_rows(const AttnMx4Args& m, bool near, bool compact, hipStream_t s) {
-  if (!near) return attn_keys_mx4_go<T, DP, RT, 0, false, kWaves>(m, compact, s);
+  if (!near)
+    return m.a.p.D == DP ? attn_keys_mx4_go<T, DP, RT, 0, true, kWaves>(m, compact, s)
+                         : attn_keys_mx4_go<T, DP, RT, 0, false, kWaves>(m, compact, s);
   return m.a.p.D == DP ? attn_keys_mx4_go<T, DP, RT, 16, true, kWaves>(m, compact, s)
                        : attn_keys_mx4_go<T, DP, RT, 16, false, kWaves>(m, compact, s);
 }

@@ -35,9 +35,9 @@ hipError_t launch(AttnMx4Args m, const Plan& keys, const Plan& rows, void* ws, h
   const int dtype = sizeof(T) == 2 ? 1 : 0;
   // see RowPlace
   const Mx4Rows &k = m.k, &v = m.v;
-  const bool alike = k.page == v.page && k.token == v.token && k.s_page == v.s_page && k.s_token == v.s_token;
-  const bool small = k.token < (1 << 24) && k.s_token < (1 << 24) && k.page < (1ll << 31) && k.s_page < (1ll << 31);
-  const bool near = a.p.page_size % 16 == 0 && alike && small;
+  m.alike = k.page == v.page && k.token == v.token && k.s_page == v.s_page && k.s_token == v.s_token &&
+            k.token < (1 << 24) && k.s_token < (1 << 24) && k.page < (1ll << 31) && k.s_page < (1ll << 31);
+  const bool near = a.p.page_size % 16 == 0 && m.alike;
   hipError_t e = hipSuccess;
   if (rows.used) {
     place(&a, rows, (char*)ws + keys.bytes);
@@ -68,7 +68,7 @@ bool plan_paged_attn_mx4(int dtype, const PagedAttn& p, size_t* bytes) {
 hipError_t launch_paged_attn_mx4(int dtype, const PagedAttn& p, const Mx4Rows& k, const Mx4Rows& v,
                                  void* ws, hipStream_t stream) {
   const Plan keys = keys_of(dtype, p), rows = rows_of(dtype, p, keys);
-  const AttnMx4Args m = {attn_args(p), k, v, FastDiv::make(p.hkv), {}};
+  const AttnMx4Args m = {attn_args(p), k, v, FastDiv::make(p.hkv), {}, 0};
   return dtype == 1 ? launch<uint16_t>(m, keys, rows, ws, stream)
                     : launch<float>(m, keys, rows, ws, stream);
 }
