@@ -138,9 +138,9 @@ inline void place(AttnArgs* a, const Plan& pl, void* ws) {
   a->n_tiles = pl.tiles;
   a->part_rows = pl.part_rows;
   // The join reads parts that were not written, too, where it does not wait for the lengths:
-  // up to this much that costs less than the wait (32 tokens over up to 4096 keys XX us
-  // instead of XX, three over up to 131000 XX and XX).
-  a->early = pl.bytes <= (size_t)32 << 20;
+  // up to this much that costs less than the wait (the join of three long sequences 4.8 us
+  // instead of 6.9; of 32 tokens 4.7 and 4.4; with 25 MB of a batch's few-row parts 6.4 and 4.9).
+  a->early = pl.bytes <= (size_t)8 << 20;
   a->part_o = (float*)ws;
   a->part_ml = (float*)((char*)ws + align256((size_t)pl.splits * pl.part_rows * a->p.D * 4));
 }

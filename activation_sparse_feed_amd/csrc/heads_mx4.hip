@@ -54,7 +54,7 @@ __device__ __forceinline__ double row_sum64(double v, int G) {
 // 2, the rest by 4; and where numbers are subnormal by 2^-149 r and, since |r x| <= 16, by
 // 2^-146 besides.  So a wave takes 64 bits only where that leaves a scale, a code or a sign
 // open, or where the mean square is near the ends of float32.  (All of k in 64 bits took
-// 131 us for 16384 tokens of 32 + 8 heads of 128, most of it conversions: now XX.)
+// 131 us for 16384 tokens of 32 + 8 heads of 128, most of it conversions: now 77.)
 template <typename T, int V> struct KeyRotation {
   float a[kPiece], b[kPiece];
   int other[kPiece / V];  // partners of V elements, from the row's start
@@ -161,7 +161,7 @@ template <typename T, int V> struct KeyRotation {
     return sure ? fmaxf(most * r * (24.f * 0x1p-24f), r * 0x1p-148f + 0x1p-145f) : INFINITY;
   }
   // The same in 64 bits, element by element from memory: what is rare keeps no registers
-  // (unrolled it took 115 instead of 74, and 16384 tokens 83 us instead of 75).
+  // (unrolled it took 115 instead of 74, and 16384 tokens 86 us instead of 77).
   __device__ __forceinline__ void apply64(const HeadsFwd& p, int G, const T* row, int at, bool live, int pos,
                                           float (&o)[kPiece]) const {
     double r = 1.0;
@@ -222,9 +222,7 @@ __device__ __forceinline__ void store_block(uint8_t* codes, uint8_t* scales, con
 
 // Rows of k and v of token t into the cache, from key head h0 on, kGroups times 64 / G heads,
 // G lanes a row.  All loads of a wave are under way before its arithmetic.
-constexpr int kGroups = 2;
-
-template <typename T, int V>
+template <typename T, int V, int kGroups>
 __device__ __forceinline__ void store_rows(const HeadsFwd& p, const Mx4Rows& kc, const Mx4Rows& vc, int t, int h0,
                                            int G) {
   const int lane = lane_id(), u = lane & (G - 1), at = u * kPiece, rows = kWave / G, sub = lane / G;
@@ -297,14 +295,14 @@ __device__ __forceinline__ void store_rows(const HeadsFwd& p, const Mx4Rows& kc,
 
 // A token a wave: parts of q, then of k and v.  The parts of a token run side by side: those
 // of q wait for memory, those of k and v are mostly arithmetic.
-template <typename T, int V>
+template <typename T, int V, int kGroups>
 __global__ __launch_bounds__(kHeadsBlock) void heads_mx4(HeadsFwd p, Mx4Rows k, Mx4Rows v, int q_parts, int G) {
   const int group = (int)(blockIdx.z * gridDim.y + blockIdx.y);
   const int t = uniform(group * (kHeadsBlock / kWave) + (int)threadIdx.x / kWave);
   if (t >= p.T) return;
   const int part = (int)blockIdx.x, kv = part - q_parts;
   if (kv < 0) heads_fwd_part<T, V, true>(p, t, part);
-  else store_rows<T, V>(p, k, v, t, kv * kGroups * (kWave / G), G);
+  else store_rows<T, V, kGroups>(p, k, v, t, kv * kGroups * (kWave / G), G);
 }
 
 // Rows back as values: G lanes a row, eight elements of K and of V each.
@@ -339,9 +337,12 @@ __global__ __launch_bounds__(256) void mx4_read(Mx4Read p, int G) {
 }
 
 template <typename T, int V>
-hipError_t append(const HeadsFwd& p, const Mx4Rows& k, const Mx4Rows& v, int q_parts, int G, dim3 grid,
-                  hipStream_t stream) {
-  hipLaunchKernelGGL((heads_mx4<T, V>), grid, dim3(kHeadsBlock), 0, stream, p, k, v, q_parts, G);
+hipError_t append(const HeadsFwd& p, const Mx4Rows& k, const Mx4Rows& v, int q_parts, int G, int groups,
+                  dim3 grid, hipStream_t stream) {
+  if (groups == 1)
+    hipLaunchKernelGGL((heads_mx4<T, V, 1>), grid, dim3(kHeadsBlock), 0, stream, p, k, v, q_parts, G);
+  else
+    hipLaunchKernelGGL((heads_mx4<T, V, 2>), grid, dim3(kHeadsBlock), 0, stream, p, k, v, q_parts, G);
   return hipGetLastError();
 }
 
@@ -357,16 +358,17 @@ hipError_t launch_heads_mx4(int dtype, HeadsFwd p, Mx4Rows k, Mx4Rows v, hipStre
   const int q_parts = p.hq == 0 ? 0 : (q_passes + q_each - 1) / q_each;
   int G = 4;  // lanes of a row of k or v: whole blocks
   while (G * kPiece < p.D) G *= 2;
-  const int heads = kGroups * kWave / G, groups = (p.T + 3) / 4, most = 1 << 15;
-  const dim3 grid((unsigned)(q_parts + (p.hkv + heads - 1) / heads), (unsigned)(groups < most ? groups : most),
-                  (unsigned)((groups + most - 1) / most));
+  // k and v: few tokens, a wave for every 64 / G heads, too
+  const int n = p.T < 2048 ? 1 : 2, heads = n * kWave / G, fours = (p.T + 3) / 4, most = 1 << 15;
+  const dim3 grid((unsigned)(q_parts + (p.hkv + heads - 1) / heads), (unsigned)(fours < most ? fours : most),
+                  (unsigned)((fours + most - 1) / most));
   if (dtype == 1) {
-    if (V == 8) return append<uint16_t, 8>(p, k, v, q_parts, G, grid, stream);
-    if (V == 4) return append<uint16_t, 4>(p, k, v, q_parts, G, grid, stream);
-    return append<uint16_t, 2>(p, k, v, q_parts, G, grid, stream);
+    if (V == 8) return append<uint16_t, 8>(p, k, v, q_parts, G, n, grid, stream);
+    if (V == 4) return append<uint16_t, 4>(p, k, v, q_parts, G, n, grid, stream);
+    return append<uint16_t, 2>(p, k, v, q_parts, G, n, grid, stream);
   }
-  if (V == 4) return append<float, 4>(p, k, v, q_parts, G, grid, stream);
-  return append<float, 2>(p, k, v, q_parts, G, grid, stream);
+  if (V == 4) return append<float, 4>(p, k, v, q_parts, G, n, grid, stream);
+  return append<float, 2>(p, k, v, q_parts, G, n, grid, stream);
 }
 
 hipError_t launch_mx4_read(int dtype, const Mx4Read& p, hipStream_t stream) {
