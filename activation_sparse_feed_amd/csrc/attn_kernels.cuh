@@ -23,8 +23,8 @@
 //              179 us, 5.5 TB/s), by its chain of dependent loads and steps for
 //              few (one of 257 keys: 8.6 us).
 //   attn_join  joins the splits of a long key range: for each row the maximum of the
-//              splits' maxima, then their sums and outputs scaled to it.  8.1 us
-//              for 64 splits of three tokens, 5.1 for 32 tokens: latency.
+//              splits' maxima, then their sums and outputs scaled to it.  5.6 us
+//              for 64 splits of three tokens, 5.3 for 32 tokens: latency.
 //
 // attn_rows of width 256 needs more than the 512 registers of a wave: 27 values (112
 // bytes a lane) go through scratch memory in bf16, 99 (352 bytes) in float32.

@@ -1,10 +1,20 @@
 // Kernels of attention over the 4-bit paged cache.  Rows, tiles, splits and their joining
 // are those of attn_kernels.cuh; what differs is how keys and values come to the matrix
 // instructions: codes and scales are loaded into registers, a tile ahead, and turned into
-// bfloat16 (or float32) there, with nothing rounded.
+// bfloat16 there, two elements an instruction at the full rate, with nothing rounded.
 //
 //   attn_rows_mx4  many rows (chunks of prompts): the tiles of attn_rows, K and V tiles
-//                  written to LDS by the threads that decode them.
+//                  written to LDS by the threads that decode them, a 16-byte run of codes of a
+//                  row a thread (width 128).  Bound by the matrix cores at the clock that
+//                  the card's power allows, like attn_rows: 2.06 ms for a 16384-token
+//                  prompt (32 heads on 8, width 128, bf16: 2.20 TFLOP, 1.07 PFLOP/s) where attn_rows
+//                  takes 2.21; the decoding hides beside the matrix instructions.
+//                  Eight waves (256 rows, half the decoding a row) gave 2.22 beside 2.26, but
+//                  719 us instead of 694 for chunks beside single tokens: not kept.  Both widths
+//                  of loads in one instance, chosen at run time, made its loads wait where the two
+//                  join: 744 us instead of 674.  float32: 122 us for 2048 tokens (16 heads on
+//                  4, width 128), 295 on the float32 matrix instructions.  Width 256 spills (270
+//                  bytes a lane in bf16, 860 in float32) and runs at 400 TFLOP/s.
 //   attn_keys_mx4  few rows (single tokens, drafts): tiles of 16 rows on 16x16
 //                  instructions.  A wave holds S^T [key, row] = K Q^T; lane l has the key
 //                  (as operand) or row (as result) l % 16.  The head's elements are split
@@ -14,7 +24,13 @@
 //                  128, one MX block with one scale).  So K goes from memory to the
 //                  matrix instruction in registers.  V has to be transposed: it is decoded
 //                  the same way, written to the wave's LDS as rows of values and read
-//                  with transposing loads.
+//                  with transposing loads.  Bound by HBM for long sequences (three of 31191 to
+//                  131000 keys, 261 MB: 44 us where the Infinity Cache helps, 52 without, 5.0
+//                  TB/s), by its start, six steps a wave and its end for a batch (32 tokens
+//                  over 196 to 4096 keys, 70 MB: 19 us), by its chain of loads for one token (257
+//                  keys 5.9 us).  Scalar page lookups and constant lane offsets took 75 to 69
+//                  us and 733 to 684 for chunks beside tokens; the rest of the way was the code
+//                  registers (see the loop).
 #pragma once
 
 #include "attn_kernels.cuh"
@@ -87,7 +103,7 @@ __device__ __forceinline__ void split_parts(const float (&x)[2 * N], uint32_t (&
 
 // ------------------------------------------------------------------ many rows
 // Where a row of codes and its scales lie.
-//   G = 16  page_size is a multiple of 16 and the caches are alike: a wave's 16 (or 8)
+//   G = 16  page_size is a multiple of 16 and the caches are alike: a wave's 16
 //           neighbouring rows lie in one page, which is looked up with scalar instructions,
 //           and a lane adds an offset that never changes.
 //   G = 0   any page size and strides: a lane looks up its own row.
@@ -130,7 +146,7 @@ struct Mx4Loader {
   static constexpr int kParts = Tile::kRowElems / kPer;  // threads of a row
   static constexpr int kW = kPer / 8;
   static constexpr int kB = kPer < kMxBlock ? 1 : kPer / kMxBlock;
-  static_assert(kPer % 8 == 0 && kPer * kParts == Tile::kRowElems && kWave / kParts <= 16, "");
+  static_assert(kPer % 8 == 0 && kPer * kParts == Tile::kRowElems && kWave / kParts == 16, "");
   const int32_t* bt;
   const uint8_t *codes, *scales;  // of the key head
   int64_t page_bytes, token_bytes, s_page, s_token;
@@ -154,15 +170,8 @@ struct Mx4Loader {
     first = lo, last = hi - 1;
     D = a.p.D;
   }
-  // A wave of eight rows looks up the sixteen around them.
   __device__ __forceinline__ void look_up(int j0) {
-    if constexpr (G > 0) {
-      constexpr int kRows = kWave / kParts;
-      at.look_up(bt, per_page, j0 + uniform(row) / 16 * 16, first, last);
-      if constexpr (kRows < 16) at.off += uniform(row) % 16;
-    } else {
-      at.look_up(bt, per_page, j0 + row, first, last);
-    }
+    at.look_up(bt, per_page, j0 + (G > 0 ? uniform(row) : row), first, last);
   }
   __device__ __forceinline__ void start() {
     const uint8_t* c = codes + at.bytes(last_page, page_bytes, token_bytes) + lane_codes;
@@ -170,17 +179,30 @@ struct Mx4Loader {
     load_codes<kW, WHOLE>(c, WHOLE ? 0 : part * kPer, D, w);
     load_scales<kB, WHOLE>(b, WHOLE ? 0 : part * kPer / kMxBlock, mx_blocks(D), s);
   }
-  __device__ __forceinline__ void finish(uint8_t* tile) const {
+  // Eight neighbouring threads, two rows' parts, write 16 bytes each at a time: their words
+  // go in an order of their own, so that the eight lie in different banks (in the same
+  // order 40% of the LDS cycles were conflicts, 2.15 ms instead of 2.06 for a 16384-token prompt).
+  __device__ __forceinline__ void finish(uint8_t* tile) {
+    const int odd = row & 1;
+    const int first = kW == 2 ? (K ? 0 : odd) : kW == 4 ? (part & 2) | (K ? 0 : odd) : K ? part * 2 : part;
+#pragma unroll
+    for (int bit = 1; bit < kW; bit *= 2)
+#pragma unroll
+      for (int i = 0; i < kW; ++i)
+        if ((i & bit) == 0) {
+          const uint32_t x = w[i], y = w[i | bit];
+          w[i] = first & bit ? y : x;
+          w[i | bit] = first & bit ? x : y;
+        }
     const int swz = K ? Tile::swz_k(row) : Tile::swz_v(row);
+    const int at = row * Tile::kPitch + (((part * kW + first) ^ swz) << 4);  // of word `first`
 #pragma unroll
     for (int i = 0; i < kW; ++i) {
-      u32x4_t x[Mx<T>::kChunks];
-      Mx<T>::decode8(w[i], mx_scale(s[i / 4 < kB ? i / 4 : 0]), x);
-#pragma unroll
-      for (int j = 0; j < Mx<T>::kChunks; ++j) {
-        const int c = (part * kW + i) * Mx<T>::kChunks + j;
-        *(u32x4_t*)(tile + row * Tile::kPitch + ((c ^ swz) << 4)) = x[j];
-      }
+      u32x4_t x[1];
+      // a thread's words have one scale, or (width 256) two, of four each
+      const uint32_t b = kB == 1 ? s[0] : (i ^ first) & 4 ? s[kB - 1] : s[0];
+      Mx<T>::decode8(w[i], mx_scale(b), x);
+      *(u32x4_t*)(tile + (at ^ (i << 4))) = x[0];
     }
   }
 };

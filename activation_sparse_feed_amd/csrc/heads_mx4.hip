@@ -1,4 +1,11 @@
 // Writing keys and values into the 4-bit paged cache, and reading them back.
+//
+// heads_mx4: a wave takes a token's heads of q (as in heads_fwd) or of k and v.  At 16384
+// tokens of 32 + 8 heads of 128, bf16: 71 to 77 us for 362 MB (4.7 to 5.1 TB/s; a large copy
+// runs at 4.9).  q waits for memory, k and v are arithmetic (about 31 of 55 us of it), so
+// both run side by side: one after the other took 89 us.  32 tokens 4.9 us, dependent
+// loads (position, angles) and code that is fetched once.  mx4_read: 18 us for 85 MB (4.7
+// TB/s), 3.6 us for 77 rows.
 #include <hip/hip_runtime.h>
 
 #include "attn.h"

@@ -625,9 +625,12 @@ typedef struct {
 /*
  * paged_kv_append_mx4 -- paged_kv_append into a 4-bit cache, one launch: q normalised and
  * rotated into q_out, k normalised, rotated and quantised into k_cache, v quantised
- * into v_cache.  The norm and rotation of k are computed in 64 bits and rounded to
+ * into v_cache.  The norm and rotation of k are as computed in 64 bits and rounded to
  * float32 before they are quantised, so that what is stored for a token does not depend
- * on the call that stores it.  Arguments and refusals as for paged_kv_append.
+ * on the call that stores it.  A position outside the table makes the blocks with rotated
+ * elements NaN.  Two tokens with one slot: what is kept is not specified, nor that a
+ * block's scale and elements are of the same token.  Arguments and refusals as for
+ * paged_kv_append.
  */
 int32_t paged_kv_append_mx4(const sffn_heads* heads, const void* q, int64_t q_token, int64_t q_head,
                             const void* k, int64_t k_token, int64_t k_head, const void* v,
@@ -651,9 +654,9 @@ int32_t paged_kv_read_mx4(int32_t T, int32_t n_kv_heads, int32_t head_dim, int32
 
 /*
  * paged_attn_mx4_fwd -- paged_attn_fwd over a 4-bit cache: the same batches, masks,
- * results, bounds and bits every time, over the values that the cache stands for.  q, out
- * and the arithmetic are of batch->dtype (float32 or bfloat16).  A NaN block of values that a
- * row sees makes those elements of its result NaN, one of keys all of them.
+ * results, bounds and bits every time, over the values that the cache stands for.  q and out
+ * are of batch->dtype (float32 or bfloat16), and the products as exact as it is.  A NaN block
+ * of values that a row sees makes those elements of its result NaN, one of keys all of them.
  * workspace: at least paged_attn_mx4_workspace_bytes(batch), no initial contents.
  */
 int32_t paged_attn_mx4_fwd(const sffn_paged_batch* batch, const void* q, int64_t q_token,
