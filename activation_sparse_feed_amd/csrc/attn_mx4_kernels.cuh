@@ -6,15 +6,16 @@
 //   attn_rows_mx4  many rows (chunks of prompts): the tiles of attn_rows, K and V tiles
 //                  written to LDS by the threads that decode them, a 16-byte run of codes of a
 //                  row a thread (width 128).  Bound by the matrix cores at the clock that
-//                  the card's power allows, like attn_rows: 2.06 ms for a 16384-token
-//                  prompt (32 heads on 8, width 128, bf16: 2.20 TFLOP, 1.07 PFLOP/s) where attn_rows
-//                  takes 2.21; the decoding hides beside the matrix instructions.
+//                  the card's power allows, like attn_rows: 2.06 to 2.10 ms for a 16384-token
+//                  prompt (32 heads on 8, width 128, bf16: 2.20 TFLOP, 1.05 to 1.07 PFLOP/s) where
+//                  attn_rows takes 2.21 to 2.28; the decoding hides beside the matrix instructions.
 //                  Eight waves (256 rows, half the decoding a row) gave 2.22 beside 2.26, but
 //                  719 us instead of 694 for chunks beside single tokens: not kept.  Both widths
 //                  of loads in one instance, chosen at run time, made its loads wait where the two
 //                  join: 744 us instead of 674.  float32: 122 us for 2048 tokens (16 heads on
-//                  4, width 128), 295 on the float32 matrix instructions.  Width 256 spills (270
-//                  bytes a lane in bf16, 860 in float32) and runs at 400 TFLOP/s.
+//                  4, width 128), 295 on the float32 matrix instructions.  Width 256 spills (236
+//                  to 296 bytes a lane in bf16, 804 to 896 in float32; float32 at 192 240) and runs
+//                  at 400 TFLOP/s in bf16.
 //   attn_keys_mx4  few rows (single tokens, drafts): tiles of 16 rows on 16x16
 //                  instructions.  A wave holds S^T [key, row] = K Q^T; lane l has the key
 //                  (as operand) or row (as result) l % 16.  The head's elements are split
@@ -181,7 +182,8 @@ struct Mx4Loader {
   }
   // Eight neighbouring threads, two rows' parts, write 16 bytes each at a time: their words
   // go in an order of their own, so that the eight lie in different banks (in the same
-  // order 40% of the LDS cycles were conflicts, 2.15 ms instead of 2.06 for a 16384-token prompt).
+  // order 270 of 675 M LDS cycles were conflicts, now none: 2.15 -> 2.09 ms for a 16384-token
+  // prompt, but 664 -> 673 us for chunks beside single tokens).
   __device__ __forceinline__ void finish(uint8_t* tile) {
     const int odd = row & 1;
     const int first = kW == 2 ? (K ? 0 : odd) : kW == 4 ? (part & 2) | (K ? 0 : odd) : K ? part * 2 : part;
