@@ -6,8 +6,8 @@
 //   attn_rows_mx4  many rows (chunks of prompts): the tiles of attn_rows, K and V tiles
 //                  written to LDS by the threads that decode them, a 16-byte run of codes of a
 //                  row a thread (width 128).  Bound by the matrix cores at the clock that
-//                  the card's power allows, like attn_rows: 2.06 to 2.10 ms for a 16384-token
-//                  prompt (32 heads on 8, width 128, bf16: 2.20 TFLOP, 1.05 to 1.07 PFLOP/s) where
+//                  the card's power allows, like attn_rows: 2.06 to 2.15 ms for a 16384-token
+//                  prompt (32 heads on 8, width 128, bf16: 2.20 TFLOP, 1.02 to 1.07 PFLOP/s) where
 //                  attn_rows takes 2.21 to 2.28; the decoding hides beside the matrix instructions.
 //                  Eight waves (256 rows, half the decoding a row) gave 2.22 beside 2.26, but
 //                  719 us instead of 694 for chunks beside single tokens: not kept.  Both widths
