@@ -18,7 +18,13 @@ int tile_of(int dtype, const PagedAttn& p) {
   return keys_mx4_rows(dtype == 1 ? 2 : 4, p.D, p.max_q * (int64_t)(p.hq / p.hkv));
 }
 int waves_of(int dtype, const PagedAttn& p) {
-  return keys_mx4_waves(dtype == 1 ? 2 : 4, key_span(p, keys_max(p) / (p.hq / p.hkv) + 1));
+  const int64_t g = p.hq / p.hkv, limit = keys_max(p), rows = p.max_q * g < limit ? p.max_q * g : limit;
+  const int64_t tile = tile_of(dtype, p), tiles = (rows + tile - 1) / tile, groups = (int64_t)p.n_seqs * p.hkv;
+  // A sequence of up to 32 rows has two tiles of 16 where it has one in attn_keys: a grid of
+  // them with eight waves has 2^32 threads at half the sequences.  They get four from there on,
+  // whose grid takes as many sequences as that of one tile with eight.
+  if (tiles > 1 && groups * tiles * 8 * kWave >= 1ll << 32) return 4;
+  return keys_mx4_waves(dtype == 1 ? 2 : 4, key_span(p, limit / g + 1));
 }
 Plan keys_of(int dtype, const PagedAttn& p) {
   const int step = waves_of(dtype, p) * 32, tile = tile_of(dtype, p);
