@@ -1,0 +1,61 @@
+"""Bytes of a 4-bit cache that no row sees cost attention no time."""
+from __future__ import annotations
+
+import time
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _median_us(call, n=20):
+    times = []
+    for _ in range(n):
+        torch.cuda.synchronize()
+        t = time.perf_counter()
+        call()
+        torch.cuda.synchronize()
+        times.append(time.perf_counter() - t)
+    return sorted(times)[n // 2] * 1e6
+
+
+@pytest.mark.parametrize("where", ["behind the end", "before the window"])
+def test_nan_scales_out_of_sight(where):
+    """One token over 2^20 keys, a NaN scale byte in the first or the last page, where no row
+    sees it: the same bits, and less than 1.4 times the time (it took twice the time where the
+    byte made a wave go over its keys again)."""
+    from activation_sparse_feed_amd import sffn
+    page, n_pages, hq, D = 16, 1 << 16, 4, 128
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    cache = sffn.Mx4Cache(n_pages, page, 1, D)
+    for t in (cache.k_codes, cache.v_codes):
+        t.random_(0, 256, generator=g)
+    for t in (cache.k_scales, cache.v_scales):
+        t.fill_(127)
+    n, window = n_pages * page - 3, 0
+    if where == "before the window":
+        window = n - 5
+    b = sffn.make_paged_batch(1, 1, hq, 1, D, torch.bfloat16, page, n_pages, n_pages, 1, n, window=window)
+    q = torch.randn((1, hq, D), generator=g, device="cuda").to(torch.bfloat16)
+    out, ws = torch.empty_like(q), sffn.alloc_paged_mx4_workspace(b)
+    qs = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    kv = torch.tensor([n], dtype=torch.int32, device="cuda")
+    bt = torch.arange(n_pages, dtype=torch.int32, device="cuda")[None, :]
+
+    def call():
+        sffn.paged_attn_mx4_fwd(b, q, cache, qs, kv, bt, out, ws)
+
+    call()
+    clean_us, clean = _median_us(call), out.clone()
+    stale = (n_pages - 1, page - 1) if where == "behind the end" else (0, 2)
+    cache.v_scales[stale] = 255
+    call()
+    stale_us = _median_us(call)
+    assert torch.equal(out, clean)
+    assert stale_us < 1.4 * clean_us, (stale_us, clean_us)
+    # where the row sees the byte, its block is NaN
+    cache.v_scales[n_pages // 2, 3] = 255
+    call()
+    assert torch.isnan(out).all()
