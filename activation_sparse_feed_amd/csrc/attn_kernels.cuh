@@ -23,8 +23,8 @@
 //              179 us, 5.5 TB/s), by its chain of dependent loads and steps for
 //              few (one of 257 keys: 8.6 us).
 //   attn_join  joins the splits of a long key range: for each row the maximum of the
-//              splits' maxima, then their sums and outputs scaled to it.  5.6 us
-//              for 64 splits of three tokens, 5.3 for 32 tokens: latency.
+//              splits' maxima, then their sums and outputs scaled to it.  4.9 us
+//              for 64 splits of three tokens, 4.7 for 32 tokens: latency.
 //
 // attn_rows of width 256 needs more than the 512 registers of a wave: 27 values (112
 // bytes a lane) go through scratch memory in bf16, 99 (352 bytes) in float32.
@@ -575,8 +575,11 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys(AttnArgs
 // hold the maxima and sums of up to 64 splits, then D / 4 lanes a split's outputs,
 // several splits side by side.  attn_keys' rows are few and may have many splits:
 // the four waves of a workgroup share a row; otherwise each has its own.
-template <typename T, int TM>
+// EARLY (of attn_keys): the first row's parts are loaded before their number is known, those
+// that were not written, too, and are dropped.
+template <typename T, int TM, bool EARLY>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
+  static_assert(TM == 32 || !EARLY, "");
   constexpr int kShare = TM == 32 ? 4 : 1;  // waves of a row
   constexpr int kAhead = 8;                 // loads of a lane in flight
   __shared__ f32x4_t sums[kShare][kWave];
@@ -594,18 +597,20 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   const int i_first = kShare == 4 ? (int)blockIdx.y : (int)blockIdx.y * 4 + wave;
   const float* const outputs = a.part_o + (d < p.D ? d : 0);
   float m_ahead = -INFINITY, l_ahead = 0.f;
-  f32x4_t o_ahead[kAhead];
-  const bool early = a.early != 0 && (TM == 32 ? tile_row + i_first < a.slot_rows : i_first < TM);
-  if (early) {
-    const size_t slot = slots + i_first;
-    const size_t at = (size_t)min(lane, a.splits - 1) * a.part_rows + slot;
-    m_ahead = a.part_ml[2 * at];
-    l_ahead = a.part_ml[2 * at + 1];
+  f32x4_t o_ahead[EARLY ? kAhead : 1];
+  const bool there = EARLY && tile_row + i_first < a.slot_rows;
+  if constexpr (EARLY) {
+    if (there) {
+      const size_t slot = slots + i_first;
+      const size_t at = (size_t)min(lane, a.splits - 1) * a.part_rows + slot;
+      m_ahead = a.part_ml[2 * at];
+      l_ahead = a.part_ml[2 * at + 1];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (s_first + k * s_step < a.splits)
-        o_ahead[k] = *(const f32x4_t*)(outputs + ((size_t)min(s_first + k * s_step + sub, a.splits - 1) *
-                                                  a.part_rows + slot) * p.D);
+      for (int k = 0; k < kAhead; ++k)
+        if (s_first + k * s_step < a.splits)
+          o_ahead[k] = *(const f32x4_t*)(outputs + ((size_t)min(s_first + k * s_step + sub, a.splits - 1) *
+                                                    a.part_rows + slot) * p.D);
+    }
   }
   Work w;
   int n;
@@ -632,7 +637,7 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   if (n == 1) return;  // written by the kernel before
   for (int i = i_first; r0 + i <= r1; i += (int)gridDim.y * (4 / kShare)) {
     const int r = r0 + i;
-    const bool ahead = early && i == i_first;
+    const bool ahead = EARLY && there && i == i_first;
     const size_t slot = slots + i;
     float ms = -INFINITY, ls = 0.f;
     if (lane < n) {
@@ -655,11 +660,13 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
       for (int i = 0; i < 4; ++i) v[i] += s < n ? fs * x[i] : 0.f;
     };
     int s0 = s_first;
-    if (ahead) {
+    if constexpr (EARLY) {
+      if (ahead) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (s_first + k * s_step < n) add(s_first + k * s_step, o_ahead[k]);
-      s0 += kAhead * s_step;
+        for (int k = 0; k < kAhead; ++k)
+          if (s_first + k * s_step < n) add(s_first + k * s_step, o_ahead[k]);
+        s0 += kAhead * s_step;
+      }
     }
     // loads without conditions, so that they are in flight together
 #pragma unroll 8

@@ -137,10 +137,6 @@ inline void place(AttnArgs* a, const Plan& pl, void* ws) {
   a->splits = pl.splits;
   a->n_tiles = pl.tiles;
   a->part_rows = pl.part_rows;
-  // The join reads parts that were not written, too, where it does not wait for the lengths:
-  // up to this much that costs less than the wait (the join of three long sequences 4.8 us
-  // instead of 6.9; of 32 tokens 4.7 and 4.4; with 25 MB of a batch's few-row parts 6.4 and 4.9).
-  a->early = pl.bytes <= (size_t)8 << 20;
   a->part_o = (float*)ws;
   a->part_ml = (float*)((char*)ws + align256((size_t)pl.splits * pl.part_rows * a->p.D * 4));
 }
@@ -166,8 +162,20 @@ inline AttnArgs attn_args(const PagedAttn& p) {
   return a;
 }
 
-// attn_join for the rows of kRowsTile or kKeysTile.
-hipError_t launch_attn_join(int dtype, int tile_rows, const AttnArgs& a, dim3 grid, hipStream_t s);
+// attn_join for the rows of kRowsTile or kKeysTile; early: see there.
+hipError_t launch_attn_join(int dtype, int tile_rows, bool early, const AttnArgs& a, dim3 grid, hipStream_t s);
+
+// Whether the join of attn_keys' rows loads early, which spares it a wait for the lengths but takes 80
+// registers instead of 44.  Early / late, in us, bf16, width 128, 32 heads on 8:
+//   splits of a row  64 (three tokens over up to 131072 keys) 4.9 / 7.6, 43 4.6 / 5.2, 22 (8 tokens) 4.8 / 4.9;
+//                    from 8 to 16 as fast, but 32 tokens 5.2 / 5.0; 6 5.1 / 4.7, 4 4.9 / 4.7
+//   workgroups       1024 (32 tokens, 22 splits) 5.9 / 6.2, 2048 (64) 8.8 / 7.5, 8192 (256, 6) 16.3 / 13.3
+//   bytes of parts   where max_kv is far above the lengths, hardly any of those that are read were
+//                    written: 32 tokens over up to 4096 keys, max_kv 131072, 34 MB 8.8 / 4.8, 8 tokens
+//                    8.5 MB 4.3 / 4.2
+inline bool join_early(const Plan& pl, dim3 grid) {
+  return pl.splits > 16 && (int64_t)grid.x * grid.y <= 1024 && pl.bytes <= (size_t)8 << 20;
+}
 
 // The join of the splits of one of the two kernels, where there are any.  Rows of attn_keys
 // are joined by 32, whatever its tiles.
@@ -175,10 +183,11 @@ inline hipError_t launch_join(int dtype, int tile_rows, AttnArgs a, const Plan& 
   if (pl.splits <= 1) return hipSuccess;
   const PagedAttn& p = a.p;
   if (tile_rows != kKeysTile)
-    return launch_attn_join(dtype, tile_rows, a, join_grid(pl.tiles * p.hkv, tile_rows / 4, 1024), s);
+    return launch_attn_join(dtype, tile_rows, false, a, join_grid(pl.tiles * p.hkv, tile_rows / 4, 1024), s);
   a.tiles_per_seq = (pl.slot_rows + kKeysTile - 1) / kKeysTile;
   const int rows = pl.slot_rows < kKeysTile ? pl.slot_rows : kKeysTile;
-  return launch_attn_join(dtype, tile_rows, a, join_grid(p.n_seqs * a.tiles_per_seq * p.hkv, rows, 4096), s);
+  const dim3 grid = join_grid(p.n_seqs * a.tiles_per_seq * p.hkv, rows, 4096);
+  return launch_attn_join(dtype, tile_rows, join_early(pl, grid), a, grid, s);
 }
 
 }  // namespace sffn

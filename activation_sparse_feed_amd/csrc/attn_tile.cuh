@@ -70,7 +70,6 @@ struct AttnArgs {
   float* part_o;         // [split][slot][D] outputs before the division, for split rows
   float* part_ml;        // [split][slot][2] maximum (base 2) and sum
   size_t part_rows;      // slots of one split
-  int early;             // attn_join: loads its first row's parts before it knows their number
 };
 
 // ------------------------------------------------------------------ arithmetic

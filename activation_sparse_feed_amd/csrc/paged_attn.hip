@@ -58,16 +58,17 @@ hipError_t launch(AttnArgs a, const Plan& keys, const Plan& rows, void* ws, hipS
 }
 
 template <typename T>
-void join(int tile_rows, const AttnArgs& a, dim3 grid, hipStream_t s) {
-  if (tile_rows == kKeysTile) hipLaunchKernelGGL((attn_join<T, kKeysTile>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((attn_join<T, kRowsTile>), grid, dim3(256), 0, s, a);
+void join(int tile_rows, bool early, const AttnArgs& a, dim3 grid, hipStream_t s) {
+  if (tile_rows != kKeysTile) hipLaunchKernelGGL((attn_join<T, kRowsTile, false>), grid, dim3(256), 0, s, a);
+  else if (early) hipLaunchKernelGGL((attn_join<T, kKeysTile, true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((attn_join<T, kKeysTile, false>), grid, dim3(256), 0, s, a);
 }
 
 }  // namespace
 
-hipError_t launch_attn_join(int dtype, int tile_rows, const AttnArgs& a, dim3 grid, hipStream_t s) {
-  if (dtype == 1) join<uint16_t>(tile_rows, a, grid, s);
-  else join<float>(tile_rows, a, grid, s);
+hipError_t launch_attn_join(int dtype, int tile_rows, bool early, const AttnArgs& a, dim3 grid, hipStream_t s) {
+  if (dtype == 1) join<uint16_t>(tile_rows, early, a, grid, s);
+  else join<float>(tile_rows, early, a, grid, s);
   return hipGetLastError();
 }
 
