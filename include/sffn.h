@@ -574,7 +574,9 @@ typedef struct {
  * see may hold anything, NaN included: they do not change its result.  An
  * infinite or NaN element of a value that it sees makes that element of its
  * result infinite or NaN (NaN for an infinite one whose weight is below
- * float32's range).
+ * float32's range).  Sums are taken before the division, with weights of up to 2^8: where
+ * the magnitudes of an element over the keys that a row sees sum to 2^119 or more, its result
+ * may be infinite or NaN though the mean is not.
  * out: as q.  lse: float32 [T, n_q_heads] or NULL.
  * workspace: at least paged_attn_workspace_bytes(batch), about 256 MiB at most
  * for each of the two kernels that a batch may take; no initial contents.
@@ -654,7 +656,8 @@ int32_t paged_kv_read_mx4(int32_t T, int32_t n_kv_heads, int32_t head_dim, int32
 
 /*
  * paged_attn_mx4_fwd -- paged_attn_fwd over a 4-bit cache: the same batches, masks,
- * results, bounds and bits every time, over the values that the cache stands for.  q and out
+ * results, bounds (that of sums, 2^119, too: a cache can hold more) and bits every time, over the
+ * values that the cache stands for.  q and out
  * are of batch->dtype (float32 or bfloat16), and the products as exact as it is.  A NaN block
  * of values that a row sees makes those elements of its result NaN, one of keys all of them.
  * workspace: at least paged_attn_mx4_workspace_bytes(batch), no initial contents.

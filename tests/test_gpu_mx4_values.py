@@ -46,7 +46,7 @@ def largest_values(c, causal=True, window=0):
     return res
 
 
-def check_values(c, out, lse, causal=True, window=0, sm_scale=None):
+def check_values(c, out, lse, causal=True, window=0, sm_scale=None, lost=None):
     T, B, hq, hkv, D = c["dims"]
     s = D ** -0.5 if sm_scale is None else sm_scale
     want, want_l, mag, smax = A.paged_attention(to_f64(c["q"]), to_f64(c["k"]), to_f64(c["v"]), c["qs"],
@@ -54,7 +54,9 @@ def check_values(c, out, lse, causal=True, window=0, sm_scale=None):
     n = int(c["kv"].max())
     rel = 2 * ((D + 2) * smax + n + 64) * U + (2 * E if c["dtype"] == "bf16" else 0.0)
     own = E if c["dtype"] == "bf16" else U
-    lost = n * 2.0 ** -125 * (1.0 + largest_values(c, causal, window))
+    if lost is None:
+        lost = n * 2.0 ** -125 * (1.0 + largest_values(c, causal, window))
+    lost = np.broadcast_to(lost, want.shape)
     rows = np.arange(T) < c["qs"][-1]
     got, got_l = to_f64(out), to_f64(lse)
     assert (got[~rows] == 7.0).all() and (got_l[~rows] == 7.0).all()
@@ -144,6 +146,19 @@ def test_values_of_all_sizes(e, q_lens, kv_lens, dtype):
     M._quantised(c)
     out, lse = M._run(c)
     check_values(c, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 70], [300, 90]), ([3, 1], [2500, 40])])
+def test_smallest_values(q_lens, kv_lens, dtype):
+    """Values of 2^-124, near the smallest that a cache holds: the matrix instructions keep
+    subnormal products to multiples of 2^-149, with a sum of weights of at least 2^-1 n 2^-148 of a
+    result, which is rounded to multiples of 2^-133 (bf16) or 2^-149."""
+    c = _attention_case(q_lens, kv_lens, 4, 2, 64, 16, dtype, seed=9)
+    c["v"] = torch.where(torch.isfinite(c["v"]), c["v"].double() * 2.0 ** -124, math.nan)
+    M._quantised(c)
+    out, lse = M._run(c)
+    check_values(c, out, lse, lost=max(kv_lens) * 2.0 ** -148 + (2.0 ** -134 if dtype == "bf16" else 2.0 ** -150))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
