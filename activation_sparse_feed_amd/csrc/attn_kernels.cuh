@@ -6,7 +6,7 @@
 //
 //   attn_rows  many rows (chunks of prompts): four waves of 32 rows each, K and V
 //              tiles shared in LDS, double buffered.  Bound by the matrix cores at the
-//              clock that the card's power allows: 2.1 to 2.2 ms for a 16384-token
+//              clock that the card's power allows: 2.15 to 2.28 ms for a 16384-token
 //              prompt (32 heads on 8, width 128, bf16: 2.20 TFLOP, so 1.0 PFLOP/s;
 //              a large library product runs at 1.14), matrix cores busy half of the
 //              cycles at 1.75 to 2.0 GHz.  In copies of this kernel for timing (2.31
@@ -23,8 +23,8 @@
 //              179 us, 5.5 TB/s), by its chain of dependent loads and steps for
 //              few (one of 257 keys: 8.6 us).
 //   attn_join  joins the splits of a long key range: for each row the maximum of the
-//              splits' maxima, then their sums and outputs scaled to it.  4.9 us
-//              for 64 splits of three tokens, 4.7 for 32 tokens: latency.
+//              splits' maxima, then their sums and outputs scaled to it.  5.0 us
+//              for 64 splits of three tokens, 4.8 for 32 tokens: latency.
 //
 // attn_rows of width 256 needs more than the 512 registers of a wave: 27 values (112
 // bytes a lane) go through scratch memory in bf16, 99 (352 bytes) in float32.

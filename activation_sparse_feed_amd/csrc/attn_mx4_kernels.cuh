@@ -6,9 +6,9 @@
 //   attn_rows_mx4  many rows (chunks of prompts): the tiles of attn_rows, K and V tiles
 //                  written to LDS by the threads that decode them, a 16-byte run of codes of a
 //                  row a thread (width 128).  Bound by the matrix cores at the clock that
-//                  the card's power allows, like attn_rows: 2.06 to 2.15 ms for a 16384-token
+//                  the card's power allows, like attn_rows: 2.06 to 2.16 ms for a 16384-token
 //                  prompt (32 heads on 8, width 128, bf16: 2.20 TFLOP, 1.02 to 1.07 PFLOP/s) where
-//                  attn_rows takes 2.21 to 2.28; the decoding hides beside the matrix instructions.
+//                  attn_rows takes 2.15 to 2.28; the decoding hides beside the matrix instructions.
 //                  Eight waves (256 rows, half the decoding a row) gave 2.22 beside 2.26, but
 //                  719 us instead of 694 for chunks beside single tokens: not kept.  Both widths
 //                  of loads in one instance, chosen at run time, made its loads wait where the two
@@ -496,7 +496,11 @@ struct KeysTile {
   }
 
   // o += V^T P^T over the 32 keys in LDS.  A lane's weights are those of the keys 4 (lane / 16)
-  // + i and 16 more: the order in which the B operand takes them when V^T is read alike.
+  // + i and 16 more: the order in which the B operand takes them when V^T is read alike.  In
+  // bf16 they are rounded to bf16 here, as in AttnTile::accumulate (their sum l is not), since the
+  // matrix instruction takes both operands in one type and two parts would be twice the products:
+  // relative error against 64 bits 2.0e-3 to 2.35e-3 where rounding the output alone gives
+  // 1.5e-3 to 1.7e-3 (standard normal inputs).  In float32 three parts keep all 24 bits.
   __device__ __forceinline__ void accumulate(const uint8_t* lds, const f32x4_t (&s)[2][RT]) {
     const int lane = lane_id(), i = lane & 15, g = lane >> 4;
     u32x4_t pf[RT][kParts];

@@ -3,8 +3,10 @@
 // heads_mx4: a wave takes a token's heads of q (as in heads_fwd) or of k and v.  At 16384
 // tokens of 32 + 8 heads of 128, bf16: 71 to 77 us for 362 MB (4.7 to 5.1 TB/s; a large copy
 // runs at 4.9).  q waits for memory, k and v are arithmetic (about 31 of 55 us of it), so
-// both run side by side: one after the other took 89 us.  32 tokens 4.9 us, dependent
-// loads (position, angles) and code that is fetched once.  mx4_read: 18 us for 85 MB (4.7
+// both run side by side: one after the other took 89 us.  Those are normed heads: keys that
+// lie right on borders between codes take 64 bits (see KeyRotation), up to 205 us where all are
+// zero, 114 for bf16 heads rotated by half without a norm (91 with one).  32 tokens 4.9 us,
+// dependent loads (position, angles) and code that is fetched once.  mx4_read: 18 us for 85 MB (4.7
 // TB/s), 3.6 us for 77 rows.
 #include <hip/hip_runtime.h>
 
@@ -61,7 +63,10 @@ __device__ __forceinline__ double row_sum64(double v, int G) {
 // 2, the rest by 4; and where numbers are subnormal by 2^-149 r and, since |r x| <= 16, by
 // 2^-146 besides.  So a wave takes 64 bits only where that leaves a scale, a code or a sign
 // open, or where the mean square is near the ends of float32.  (All of k in 64 bits took
-// 131 us for 16384 tokens of 32 + 8 heads of 128, most of it conversions: now 77.)
+// 131 us for 16384 tokens of 32 + 8 heads of 128, most of it conversions: now 77.)  That is
+// under 1% of the waves with a norm; but the bound is one for a lane's elements, exact ones
+// too: a zero has an open sign, and what is copied (from rot on without a norm) is, in bf16, often
+// right on a border, so that most waves of such heads take 64 bits.
 template <typename T, int V> struct KeyRotation {
   float a[kPiece], b[kPiece];
   int other[kPiece / V];  // partners of V elements, from the row's start

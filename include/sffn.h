@@ -657,9 +657,10 @@ int32_t paged_kv_read_mx4(int32_t T, int32_t n_kv_heads, int32_t head_dim, int32
 /*
  * paged_attn_mx4_fwd -- paged_attn_fwd over a 4-bit cache: the same batches, masks,
  * results, bounds (that of sums, 2^119, too: a cache can hold more) and bits every time, over the
- * values that the cache stands for.  q and out
- * are of batch->dtype (float32 or bfloat16), and the products as exact as it is.  A NaN block
- * of values that a row sees makes those elements of its result NaN, one of keys all of them.
+ * values that the cache stands for.  q and out are of batch->dtype (float32 or bfloat16).  In
+ * float32 the products keep its 24 bits; in bfloat16 weights are rounded to it before the product
+ * with v, as in paged_attn_fwd.  A NaN block of values that a row sees makes those elements of
+ * its result NaN, one of keys all of them.
  * workspace: at least paged_attn_mx4_workspace_bytes(batch), no initial contents.
  */
 int32_t paged_attn_mx4_fwd(const sffn_paged_batch* batch, const void* q, int64_t q_token,
