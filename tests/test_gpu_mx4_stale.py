@@ -9,15 +9,15 @@ import torch
 pytestmark = pytest.mark.gpu
 
 
-def _median_us(call, n=20):
-    times = []
+def _least_us(call, n=20):
+    least = 1e9
     for _ in range(n):
         torch.cuda.synchronize()
         t = time.perf_counter()
         call()
         torch.cuda.synchronize()
-        times.append(time.perf_counter() - t)
-    return sorted(times)[n // 2] * 1e6
+        least = min(least, time.perf_counter() - t)
+    return least * 1e6
 
 
 @pytest.mark.parametrize("where", ["behind the end", "before the window"])
@@ -48,13 +48,15 @@ def test_nan_scales_out_of_sight(where):
         sffn.paged_attn_mx4_fwd(b, q, cache, qs, kv, bt, out, ws)
 
     call()
-    clean_us, clean = _median_us(call), out.clone()
+    clean, times = out.clone(), {127: [], 255: []}
     stale = (n_pages - 1, page - 1) if where == "behind the end" else (0, 2)
-    cache.v_scales[stale] = 255
-    call()
-    stale_us = _median_us(call)
-    assert torch.equal(out, clean)
-    assert stale_us < 1.4 * clean_us, (stale_us, clean_us)
+    for _ in range(3):      # in turn
+        for byte in times:
+            cache.v_scales[stale] = byte
+            call()
+            times[byte].append(_least_us(call))
+            assert torch.equal(out, clean)
+    assert min(times[255]) < 1.4 * min(times[127]), times
     # where the row sees the byte, its block is NaN
     cache.v_scales[n_pages // 2, 3] = 255
     call()
