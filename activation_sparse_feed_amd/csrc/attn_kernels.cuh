@@ -26,8 +26,8 @@
 //              splits' maxima, then their sums and outputs scaled to it.  5.0 us
 //              for 64 splits of three tokens, 4.8 for 32 tokens: latency.
 //
-// attn_rows of width 256 needs more than the 512 registers of a wave: 27 values (112
-// bytes a lane) go through scratch memory in bf16, 99 (352 bytes) in float32.
+// attn_rows of width 256 takes a wave's 512 registers: 505 in bf16 (560 TFLOP/s at a 4096-token
+// prompt, 32 heads on 8), and 68 to 80 bytes a lane of scratch memory in float32.
 #pragma once
 
 #include "attn_tile.cuh"
@@ -380,9 +380,12 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void 
       load_k.look_up(j0 + 2 * KT + 32);
     }
     if (!(j0 >= x && j0 + KT <= y) &&  // some row of the workgroup does not see some key
-        __syncthreads_or(Tile::template find_infinite<NW * 64>(v, threadIdx.x))) {
-      tile.add_infinite(v, j0, row_lo, row_hi);
-      __syncthreads();
+        __builtin_expect(__syncthreads_or(Tile::template find_infinite<NW * 64>(v, threadIdx.x)), 0)) {
+      if (__builtin_expect(
+              __syncthreads_or(Tile::template find_infinite_in<NW * 64, 64>(v, threadIdx.x, b - j0, e - j0)), 0)) {
+        tile.add_infinite(v, j0, row_lo, row_hi);
+        __syncthreads();
+      }
       Tile::template clear_infinite<NW * 64>(v, threadIdx.x);
       __syncthreads();
     }
@@ -503,8 +506,9 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_keys(AttnArgs
       if (more) wait_one();  // V is here
       else wait_loads<0>();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      if (!whole && __any(Tile::template find_infinite<kWave>(v, lane))) {
-        tile.add_infinite(v, j0, row_lo, row_hi);
+      if (__builtin_expect(!whole && __any(Tile::template find_infinite<kWave>(v, lane)), 0)) {
+        if (__builtin_expect(__any(Tile::template find_infinite_in<kWave, 1>(v, lane, b - j0, e - j0)), 0))
+          tile.add_infinite(v, j0, row_lo, row_hi);
         Tile::template clear_infinite<kWave>(v, lane);
       }
       tile.accumulate(v, s);

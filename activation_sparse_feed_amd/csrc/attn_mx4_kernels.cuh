@@ -13,9 +13,9 @@
 //                  719 us instead of 694 for chunks beside single tokens: not kept.  Both widths
 //                  of loads in one instance, chosen at run time, made its loads wait where the two
 //                  join: 744 us instead of 674.  float32: 122 us for 2048 tokens (16 heads on
-//                  4, width 128), 295 on the float32 matrix instructions.  Width 256 spills (236
-//                  to 296 bytes a lane in bf16, 804 to 896 in float32; float32 at 192 240) and runs
-//                  at 400 TFLOP/s in bf16.
+//                  4, width 128), 295 on the float32 matrix instructions.  Width 256 spills (24
+//                  to 48 bytes a lane in bf16, 560 to 648 in float32) and runs at 590 TFLOP/s in
+//                  bf16.
 //   attn_keys_mx4  few rows (single tokens, drafts): tiles of 16 rows on 16x16
 //                  instructions.  A wave holds S^T [key, row] = K Q^T; lane l has the key
 //                  (as operand) or row (as result) l % 16.  The head's elements are split
@@ -344,8 +344,10 @@ __global__ __launch_bounds__(NW * 64, DP <= (sizeof(T) == 2 ? 128 : 64) ? 2 : 1)
     }
     if (!(j0 >= x && j0 + KT <= y) &&  // some row of the workgroup does not see some key
         __syncthreads_or(Tile::template find_infinite<NW * 64>(v, threadIdx.x))) {
-      tile.add_infinite(v, j0, pl.row_lo, pl.row_hi);
-      __syncthreads();
+      if (__syncthreads_or(Tile::template find_infinite_in<NW * 64, 1>(v, threadIdx.x, b - j0, e - j0))) {
+        tile.add_infinite(v, j0, pl.row_lo, pl.row_hi);
+        __syncthreads();
+      }
       Tile::template clear_infinite<NW * 64>(v, threadIdx.x);
       __syncthreads();
     }
